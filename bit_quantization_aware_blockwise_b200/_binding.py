@@ -18,6 +18,7 @@ CODES_PACKED, CODES_INT8, CODES_GEMM_OPERAND, CODES_GEMM_OPERAND_E4M3 = 0, 1, 2,
 CODES_FP4_PACKED, CODES_FP4_OPERAND = 4, 5   # FP4 (E2M1) grid, bits = 4
 MASK_BITS, MASK_BYTES = 0, 1
 BF16, FP32 = 0, 1
+ACT_SILU, ACT_GELU_TANH = 0, 1
 _STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "CUDA error", 4: "device wait timed out"}
 
 # Every symbol the header declares, with (restype, argtypes).
@@ -47,6 +48,13 @@ SIGNATURES = {
     "quest_quantize_sparse24": (_int, [_p, _i64, _i64, _int, _int, _i64, _f32, _p, _p, _p, _p, _p, _p]),
     "quest_alpha_sparse24": (_f64, [_int]),
     "quest_w4a4_linear_sparse24": (_int, [_p, _p, _p, _p, _p, _i64, _i64, _i64, _p, _p, _p]),
+    "quest_gated_linear": (_int, [_p, _p, _p, _i64, _i64, _i64, _int, _p, _p, _p, _p]),
+    "quest_gated_bwd": (_int, [_p, _p, _p, _i64, _i64, _int, _p, _p, _p]),
+    "quest_weight_grad": (_int, [_p, _i64, _p, _int, _int, _p, _i64, _p, _i64, _i64, _i64, _int, _p, _int, _int, _p,
+                                 _sz, _p]),
+    "quest_weight_grad_workspace": (_sz, [_i64, _i64, _i64]),
+    "quest_lowbit_linear": (_int, [_p, _i64, _p, _int, _p, _i64, _i64, _i64, _i64, _int, _p, _p]),
+    "quest_lowbit_gated": (_int, [_p, _i64, _p, _p, _p, _p, _int, _i64, _i64, _i64, _i64, _int, _int, _p, _p]),
 }
 
 # The benchmark's tensor-core rate probes (include/quest_probe.h), in their own library.
@@ -179,6 +187,39 @@ def transpose_bf16_raw(src, rows, cols, dst, stream=0):
 def w4a4_linear_grouped_raw(a_codes, a_scales, w_codes, w_scales, M, N, K, group, y, y_f32=None, stream=0):
     _check(load_library().quest_w4a4_linear_grouped(a_codes, a_scales, w_codes, w_scales, M, N, K, group, y,
                                                     y_f32, stream), "quest_w4a4_linear_grouped")
+
+
+def gated_linear_raw(x_hat, w_gate, w_up, M, F, K, act, h, ckpt_codes=None, ckpt_scales=None, stream=0):
+    _check(load_library().quest_gated_linear(x_hat, w_gate, w_up, M, F, K, act, h, ckpt_codes, ckpt_scales, stream),
+           "quest_gated_linear")
+
+
+def gated_bwd_raw(grad_h, ckpt_codes, ckpt_scales, M, F, act, grad_ab, h=None, stream=0):
+    _check(load_library().quest_gated_bwd(grad_h, ckpt_codes, ckpt_scales, M, F, act, grad_ab, h, stream),
+           "quest_gated_bwd")
+
+
+def weight_grad_raw(grad_y, ld_gy, codes, code_mode, bits, scales, rms_group, mask, T, N, K, had_block, grad_w,
+                    out_dtype, accumulate=0, workspace=None, workspace_bytes=0, stream=0):
+    _check(load_library().quest_weight_grad(grad_y, ld_gy, codes, code_mode, bits, scales, rms_group, mask, T, N, K,
+                                            had_block, grad_w, out_dtype, accumulate, workspace, workspace_bytes,
+                                            stream), "quest_weight_grad")
+
+
+def weight_grad_workspace(T: int, N: int, K: int) -> int:
+    """Bytes of workspace weight_grad_raw needs on the current device (0: none)."""
+    return int(load_library().quest_weight_grad_workspace(T, N, K))
+
+
+def lowbit_linear_raw(x, ld_x, w_codes, code_mode, w_scales, rms_group, M, N, K, had_block, y, stream=0):
+    _check(load_library().quest_lowbit_linear(x, ld_x, w_codes, code_mode, w_scales, rms_group, M, N, K, had_block, y,
+                                              stream), "quest_lowbit_linear")
+
+
+def lowbit_gated_raw(x, ld_x, gate_codes, gate_scales, up_codes, up_scales, code_mode, rms_group, M, F, K, had_block,
+                     act, h, stream=0):
+    _check(load_library().quest_lowbit_gated(x, ld_x, gate_codes, gate_scales, up_codes, up_scales, code_mode,
+                                             rms_group, M, F, K, had_block, act, h, stream), "quest_lowbit_gated")
 
 
 def device_status(stream=0):
@@ -508,6 +549,227 @@ def w4a4_linear_grouped(a_codes, a_scales, w_codes, w_scales, out=None, y_f32: b
                             M, N, K, group, out.data_ptr(), y32.data_ptr() if y32 is not None else None,
                             _stream_handle(stream, dev))
     return (out, y32) if y_f32 else out
+
+
+class _on:
+    """Runs a call on the tensors' device: with ``stream``, on that stream, allocations
+    included, so that memory freed by the caller's other streams is not written early."""
+    __slots__ = ("ctx",)
+
+    def __init__(self, device, stream):
+        torch = _torch()
+        if stream is not None:
+            if stream.device != device:
+                raise QuestError(f"stream is on {stream.device}, the tensors are on {device}")
+            self.ctx = torch.cuda.stream(stream)
+        else:
+            self.ctx = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _act(act) -> int:
+    code = {"silu": ACT_SILU, "gelu_tanh": ACT_GELU_TANH, ACT_SILU: ACT_SILU, ACT_GELU_TANH: ACT_GELU_TANH}.get(act)
+    if code is None:
+        raise QuestError(f"act must be 'silu' or 'gelu_tanh', not {act!r}")
+    return code
+
+
+def _dense(name, t, dtypes, device, shape=None, pitched=False):
+    """Checks a tensor argument: on ``device``, one of ``dtypes``, contiguous (or, ``pitched``,
+    2-D with unit column stride) and, where given, of that shape."""
+    if not t.is_cuda:
+        raise QuestError(f"{name} must be a CUDA tensor (there is no CPU path)")
+    if t.device != device:
+        raise QuestError(f"{name} is on {t.device}, not on {device}")
+    if t.dtype not in dtypes:
+        raise QuestError(f"{name} must be one of {', '.join(str(d) for d in dtypes)}, not {t.dtype}")
+    if pitched:
+        if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+            raise QuestError(f"{name} must be 2-D with unit column stride and rows that do not overlap")
+    elif not t.is_contiguous():
+        raise QuestError(f"{name} must be contiguous")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise QuestError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+
+
+def _pitch(t):
+    return t.stride(0) if t.shape[0] > 1 and t.shape[1] > 0 else t.shape[1]
+
+
+def _rms_group(name, scales, rows, K):
+    """128 or K, read off a [rows, K / rms_group] (or, one step per row, [rows]) scale tensor."""
+    if scales.numel() == rows and K != 128:
+        return K
+    if K % 128 == 0 and tuple(scales.shape) == (rows, K // 128) or scales.numel() == rows:
+        return 128
+    raise QuestError(f"{name} must be [{rows}, {K // 128}] or one step per row, not {list(scales.shape)}")
+
+
+def gated_linear(x_hat, w_gate, w_up, act="silu", checkpoint: bool = False, out=None, stream=None):
+    """h = act(x_hat @ w_gate^T) * (x_hat @ w_up^T), the gated feed-forward block up to its down
+    projection: x_hat bf16 [M, K], weights bf16 [F, K], h bf16 [M, F]; act "silu" or
+    "gelu_tanh". Returns h, or (h, checkpoint) with ``checkpoint=True``: the projections in 8 bits,
+    {"codes": int8 [M, 2F], "scales": fp32 [M, 2 ceil(F / 128)]}, the input of gated_bwd."""
+    torch = _torch()
+    _require_cuda(x_hat, "x_hat")
+    dev, bf = x_hat.device, (torch.bfloat16,)
+    if x_hat.dim() != 2 or w_gate.dim() != 2:
+        raise QuestError("x_hat [M, K] and weights [F, K] expected")
+    (M, K), F = x_hat.shape, w_gate.shape[0]
+    _dense("x_hat", x_hat, bf, dev)
+    _dense("w_gate", w_gate, bf, dev, (F, K))
+    _dense("w_up", w_up, bf, dev, (F, K))
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((M, F), dtype=torch.bfloat16, device=dev)
+        else:
+            _dense("out", out, bf, dev, (M, F))
+        codes = scales = None
+        if checkpoint:
+            codes = torch.empty((M, 2 * F), dtype=torch.int8, device=dev)
+            scales = torch.empty((M, 2 * ((F + 127) // 128)), dtype=torch.float32, device=dev)
+        gated_linear_raw(x_hat.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), M, F, K, _act(act), out.data_ptr(),
+                         codes.data_ptr() if checkpoint else None, scales.data_ptr() if checkpoint else None,
+                         _stream_handle(stream, dev))
+    return (out, {"codes": codes, "scales": scales}) if checkpoint else out
+
+
+def gated_bwd(grad_h, checkpoint, act="silu", recompute_h: bool = False, out=None, stream=None):
+    """Gradients of gated_linear's two projections from grad_h bf16 [M, F] and the 8-bit checkpoint:
+    one bf16 [M, 2F] matrix, the gate's gradient in the first F columns. With ``recompute_h``
+    returns (gradients, h), h bf16 [M, F] from the restored projections."""
+    torch = _torch()
+    _require_cuda(grad_h, "grad_h")
+    dev, bf = grad_h.device, (torch.bfloat16,)
+    if grad_h.dim() != 2:
+        raise QuestError("grad_h [M, F] expected")
+    M, F = grad_h.shape
+    _dense("grad_h", grad_h, bf, dev)
+    codes, scales = checkpoint["codes"], checkpoint["scales"]
+    _dense("checkpoint codes", codes, (torch.int8,), dev, (M, 2 * F))
+    _dense("checkpoint scales", scales, (torch.float32,), dev, (M, 2 * ((F + 127) // 128)))
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((M, 2 * F), dtype=torch.bfloat16, device=dev)
+        else:
+            _dense("out", out, bf, dev, (M, 2 * F))
+        h = torch.empty((M, F), dtype=torch.bfloat16, device=dev) if recompute_h else None
+        gated_bwd_raw(grad_h.data_ptr(), codes.data_ptr(), scales.data_ptr(), M, F, _act(act), out.data_ptr(),
+                      h.data_ptr() if recompute_h else None, _stream_handle(stream, dev))
+    return (out, h) if recompute_h else out
+
+
+def weight_grad(grad_y, codes, scales, bits: int, code_mode: int = CODES_PACKED, mask=None, K: int | None = None,
+                out_dtype=None, out=None, accumulate: bool = False, stream=None):
+    """grad_w = H (m * (grad_y^T @ x_hat)) / sqrt(128) per 128-column block, with x_hat = bf16((q + 1/2)
+    Delta) read from the layer input's saved codes: grad_y bf16 [T, N] (unit column stride),
+    codes as quantize_fwd or quantize_operands wrote them for [T, K] values (K is taken from a
+    2-D ``codes``), scales fp32 [T, K/128] or one step per token, mask = the weight's trust mask
+    bits [N, K/8] or None. Returns [N, K] in ``out_dtype`` (bfloat16 by default, or
+    float32). ``accumulate`` adds into a float32 ``out``."""
+    torch = _torch()
+    _require_cuda(grad_y, "grad_y")
+    dev = grad_y.device
+    _dense("grad_y", grad_y, (torch.bfloat16,), dev, pitched=True)
+    _dense("codes", codes, (torch.uint8, torch.int8), dev)
+    _dense("scales", scales, (torch.float32,), dev)
+    T, N = grad_y.shape
+    per = container_bits(bits) if code_mode == CODES_PACKED else 8
+    if per == 0:
+        raise QuestError("bits must be in 1..8")
+    if K is None:
+        if codes.dim() != 2 or codes.shape[0] != T:
+            raise QuestError("K is needed unless codes is 2-D with a row per token")
+        K = codes.shape[1] * 8 // per
+    K = int(K)
+    if codes.numel() < T * K * per // 8:
+        raise QuestError(f"codes must hold {K * per // 8} bytes per token")
+    group = _rms_group("scales", scales, T, K) if T > 0 else K
+    if mask is not None:
+        _dense("mask", mask, (torch.uint8, torch.int32), dev)
+        if mask.numel() * mask.element_size() < N * K // 8:
+            raise QuestError("mask must hold N * K / 8 bytes")
+    if accumulate and out is None:
+        raise QuestError("accumulate needs out")
+    dtype = out_dtype if out_dtype is not None else (out.dtype if out is not None else torch.bfloat16)
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise QuestError("out_dtype must be bfloat16 or float32")
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((N, K), dtype=dtype, device=dev)
+        else:
+            _dense("out", out, (dtype,), dev, (N, K))
+        need = weight_grad_workspace(T, N, K)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        weight_grad_raw(grad_y.data_ptr(), _pitch(grad_y), codes.data_ptr(), code_mode, bits, scales.data_ptr(), group,
+                        mask.data_ptr() if mask is not None else None, T, N, K, 128, out.data_ptr(),
+                        BF16 if dtype == torch.bfloat16 else FP32, int(accumulate),
+                        ws.data_ptr() if need else None, need, _stream_handle(stream, dev))
+    return out
+
+
+def lowbit_linear(x, w_codes, w_scales, code_mode: int = CODES_PACKED, had_block: int = 128, out=None, stream=None):
+    """y = (H x) @ w^T for up to 64 tokens, w the 4-bit codes of a weight (quantize_fwd's packed
+    codes at bits 3 or 4, or CODES_FP4_PACKED) times their steps: x bf16 [M, K] (unit
+    column stride), w_codes N * K / 2 bytes, w_scales fp32 [N, K/128] or one step per row;
+    ``had_block`` 0 if x is in the Hadamard domain already. Returns bf16 [M, N]."""
+    torch = _torch()
+    _require_cuda(x, "x")
+    dev = x.device
+    _dense("x", x, (torch.bfloat16,), dev, pitched=True)
+    M, K = x.shape
+    N = w_scales.shape[0]
+    _lowbit_weight("w", w_codes, w_scales, N, K, dev)
+    group = _rms_group("w_scales", w_scales, N, K) if N > 0 else K
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        else:
+            _dense("out", out, (torch.bfloat16,), dev, (M, N))
+        lowbit_linear_raw(x.data_ptr(), _pitch(x), w_codes.data_ptr(), code_mode, w_scales.data_ptr(), group, M, N, K,
+                          had_block, out.data_ptr(), _stream_handle(stream, dev))
+    return out
+
+
+def _lowbit_weight(name, codes, scales, rows, K, dev):
+    torch = _torch()
+    _dense(f"{name}_codes", codes, (torch.uint8, torch.int8), dev)
+    _dense(f"{name}_scales", scales, (torch.float32,), dev)
+    if codes.numel() != rows * (K // 2) and not (codes.numel() == 1 and rows * K == 0):
+        raise QuestError(f"{name}_codes must hold {K // 2} bytes for each of {rows} rows")
+
+
+def lowbit_gated(x, gate_codes, gate_scales, up_codes, up_scales, act="silu", code_mode: int = CODES_PACKED,
+                 had_block: int = 128, out=None, stream=None):
+    """h = act((H x) @ gate^T) * ((H x) @ up^T) for up to 64 tokens on the 4-bit codes of both
+    weights (arguments as lowbit_linear). Returns bf16 [M, F]."""
+    torch = _torch()
+    _require_cuda(x, "x")
+    dev = x.device
+    _dense("x", x, (torch.bfloat16,), dev, pitched=True)
+    M, K = x.shape
+    F = gate_scales.shape[0]
+    _lowbit_weight("gate", gate_codes, gate_scales, F, K, dev)
+    _lowbit_weight("up", up_codes, up_scales, F, K, dev)
+    group = _rms_group("gate_scales", gate_scales, F, K) if F > 0 else K
+    if F > 0 and _rms_group("up_scales", up_scales, F, K) != group:
+        raise QuestError("gate_scales and up_scales must have one form")
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((M, F), dtype=torch.bfloat16, device=dev)
+        else:
+            _dense("out", out, (torch.bfloat16,), dev, (M, F))
+        lowbit_gated_raw(x.data_ptr(), _pitch(x), gate_codes.data_ptr(), gate_scales.data_ptr(), up_codes.data_ptr(),
+                         up_scales.data_ptr(), code_mode, group, M, F, K, had_block, _act(act), out.data_ptr(),
+                         _stream_handle(stream, dev))
+    return out
 
 
 def _check_probe(status: int, what: str):

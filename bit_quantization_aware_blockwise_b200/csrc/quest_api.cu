@@ -48,6 +48,16 @@ quest_status injected_launch_failure(const char* where) {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Whether [p, p + pn) and [q, q + qn) share a byte.
+bool overlap(const void* p, int64_t pn, const void* q, int64_t qn) {
+    const char *a = static_cast<const char*>(p), *b = static_cast<const char*>(q);
+    return a && b && pn > 0 && qn > 0 && a < b + qn && b < a + pn;
+}
+
+bool valid_act(quest_act a) { return a == QUEST_ACT_SILU || a == QUEST_ACT_GELU_TANH; }
+
+constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
+
 bool valid_had(int hb) { return hb == 16 || hb == 32 || hb == 64 || hb == 128 || hb == 256; }
 
 // Longest row the one-RMS-per-row kernel keeps in registers: 2 passes of
@@ -425,7 +435,7 @@ static quest_status prepare_quantize(const void* x, quest_dtype x_dtype, int64_t
 
 extern "C" {
 
-int quest_version(void) { return 10000; }
+int quest_version(void) { return 10100; }
 
 double quest_alpha(int bits) {
     if (bits < 1 || bits > 8) return NAN;
@@ -806,6 +816,224 @@ quest_status quest_transpose_bf16(const void* src, int64_t rows, int64_t cols, v
     return QUEST_OK;
 }
 
+quest_status quest_gated_linear(const void* x_hat, const void* w_gate, const void* w_up, int64_t M, int64_t F,
+                                int64_t K, quest_act act, void* h, int8_t* ckpt_codes, float* ckpt_scales,
+                                void* stream) {
+    g_last_error.clear();
+    if (M < 0 || F < 0 || K < 0) return fail(QUEST_EINVAL, "M, F and K must be >= 0");
+    if (M > kMaxDim || F > kMaxDim / 2 || K > kMaxDim) return fail(QUEST_EINVAL, "M, 2 F and K must be < 2^31");
+    if (F % 16 != 0) return fail(QUEST_EINVAL, "F must be a multiple of 16");
+    if (K % 8 != 0) return fail(QUEST_EINVAL, "K must be a multiple of 8 (16-byte rows)");
+    if (!valid_act(act)) return fail(QUEST_EINVAL, "invalid act");
+    if ((ckpt_codes == nullptr) != (ckpt_scales == nullptr))
+        return fail(QUEST_EINVAL, "ckpt_codes and ckpt_scales must be given together");
+    if (M > 0 && F > 0) {
+        if (M > (int64_t(1) << 44) / F) return fail(QUEST_EINVAL, "M * F must be <= 2^44");
+        if (!h) return fail(QUEST_EINVAL, "h must be non-NULL");
+        if (K > 0 && (!x_hat || !w_gate || !w_up)) return fail(QUEST_EINVAL, "x_hat, w_gate and w_up must be non-NULL");
+        if (!aligned(h, 16) || !aligned(ckpt_codes, 16) ||
+            (K > 0 && (!aligned(x_hat, 16) || !aligned(w_gate, 16) || !aligned(w_up, 16))))
+            return fail(QUEST_EINVAL, "x_hat, w_gate, w_up, h and ckpt_codes must be 16-byte aligned");
+        if (!aligned(ckpt_scales, 4)) return fail(QUEST_EINVAL, "ckpt_scales must be 4-byte aligned");
+        const void* out[3] = {h, ckpt_codes, ckpt_scales};
+        const int64_t out_n[3] = {M * F * 2, M * F * 2, M * 2 * ((F + 127) / 128) * 4};
+        const void* in[3] = {x_hat, w_gate, w_up};
+        const int64_t in_n[3] = {M * K * 2, F * K * 2, F * K * 2};
+        for (int i = 0; i < 3; ++i) {
+            for (int j = 0; j < 3; ++j)
+                if (overlap(out[i], out_n[i], in[j], in_n[j]) || (i != j && overlap(out[i], out_n[i], out[j], out_n[j])))
+                    return fail(QUEST_EINVAL, "h, ckpt_codes and ckpt_scales must not overlap anything");
+        }
+    }
+    if (take_fault(QUEST_FAULT_LAUNCH)) return injected_launch_failure("quest_gated_linear");
+    GatedArgs a = {static_cast<const uint16_t*>(x_hat), static_cast<const uint16_t*>(w_gate),
+                   static_cast<const uint16_t*>(w_up), M, F, K, (int)act, static_cast<uint16_t*>(h), ckpt_codes,
+                   ckpt_scales};
+    cudaError_t e = launch_gated_linear(a, static_cast<cudaStream_t>(stream));
+    if (e == cudaErrorInvalidValue) return fail(QUEST_ECUDA, "quest_gated_linear: tensor map encoding failed");
+    if (e != cudaSuccess) return cuda_fail(e, "quest_gated_linear launch");
+    return QUEST_OK;
+}
+
+quest_status quest_gated_bwd(const void* grad_h, const int8_t* ckpt_codes, const float* ckpt_scales, int64_t M,
+                             int64_t F, quest_act act, void* grad_ab, void* h, void* stream) {
+    g_last_error.clear();
+    if (M < 0 || F < 0) return fail(QUEST_EINVAL, "M and F must be >= 0");
+    if (M > kMaxDim || F > kMaxDim / 2) return fail(QUEST_EINVAL, "M and 2 F must be < 2^31");
+    if (F % 16 != 0) return fail(QUEST_EINVAL, "F must be a multiple of 16");
+    if (!valid_act(act)) return fail(QUEST_EINVAL, "invalid act");
+    if (M > 0 && F > 0) {
+        if (!grad_h || !ckpt_codes || !ckpt_scales || !grad_ab)
+            return fail(QUEST_EINVAL, "grad_h, ckpt_codes, ckpt_scales and grad_ab must be non-NULL");
+        if (!aligned(grad_h, 16) || !aligned(ckpt_codes, 16) || !aligned(grad_ab, 16) || !aligned(h, 16))
+            return fail(QUEST_EINVAL, "grad_h, ckpt_codes, grad_ab and h must be 16-byte aligned");
+        if (!aligned(ckpt_scales, 4)) return fail(QUEST_EINVAL, "ckpt_scales must be 4-byte aligned");
+        const void* in[3] = {grad_h, ckpt_codes, ckpt_scales};
+        const int64_t in_n[3] = {M * F * 2, M * F * 2, M * 2 * ((F + 127) / 128) * 4};
+        for (int j = 0; j < 3; ++j)
+            if (overlap(grad_ab, M * F * 4, in[j], in_n[j]) || overlap(h, M * F * 2, in[j], in_n[j]))
+                return fail(QUEST_EINVAL, "grad_ab and h must not overlap the inputs");
+        if (overlap(grad_ab, M * F * 4, h, M * F * 2)) return fail(QUEST_EINVAL, "grad_ab and h must not overlap");
+    }
+    if (take_fault(QUEST_FAULT_LAUNCH)) return injected_launch_failure("quest_gated_bwd");
+    GatedBwdArgs a = {static_cast<const uint16_t*>(grad_h), ckpt_codes, ckpt_scales, M, F, (int)act,
+                      static_cast<uint16_t*>(grad_ab), static_cast<uint16_t*>(h)};
+    cudaError_t e = launch_gated_bwd(a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "quest_gated_bwd launch");
+    return QUEST_OK;
+}
+
+size_t quest_weight_grad_workspace(int64_t T, int64_t N, int64_t K) {
+    if (T < 0 || N < 0 || K < 0 || T > kMaxDim || N > kMaxDim || K > kMaxDim || N % 8 != 0 || K % 128 != 0) return 0;
+    return weight_grad_workspace_bytes(T, N, K);
+}
+
+quest_status quest_weight_grad(const void* grad_y, int64_t ld_gy, const void* codes, quest_code_mode code_mode,
+                               int bits, const float* scales, int64_t rms_group, const void* mask, int64_t T,
+                               int64_t N, int64_t K, int had_block, void* grad_w, quest_dtype out_dtype,
+                               int accumulate, void* workspace, size_t workspace_bytes, void* stream) {
+    g_last_error.clear();
+    if (T < 0 || N < 0 || K < 0) return fail(QUEST_EINVAL, "T, N and K must be >= 0");
+    if (T > kMaxDim || N > kMaxDim || K > kMaxDim) return fail(QUEST_EINVAL, "T, N and K must be < 2^31");
+    if (bits < 1 || bits > 8) return fail(QUEST_EINVAL, "bits must be in 1..8");
+    if (code_mode < QUEST_CODES_PACKED || code_mode > QUEST_CODES_FP4_OPERAND) return fail(QUEST_EINVAL, "invalid code_mode");
+    if (code_mode == QUEST_CODES_GEMM_OPERAND_E4M3 || code_mode == QUEST_CODES_FP4_PACKED)
+        return fail(QUEST_EUNSUPPORTED, "quest_weight_grad: codes must be packed, int8 or int8 operand codes");
+    if (code_mode == QUEST_CODES_PACKED && container_bits_of(bits) < 4)
+        return fail(QUEST_EUNSUPPORTED, "quest_weight_grad: packed codes need 4- or 8-bit containers (bits 3..8)");
+    if (!valid_had(had_block)) return fail(QUEST_EINVAL, "had_block must be 16, 32, 64, 128 or 256");
+    if (had_block != 128) return fail(QUEST_EUNSUPPORTED, "quest_weight_grad: had_block must be 128");
+    if (K % 128 != 0) return fail(QUEST_EINVAL, "K must be a multiple of 128");
+    if (N % 8 != 0) return fail(QUEST_EINVAL, "N must be a multiple of 8 (16-byte rows)");
+    if (ld_gy < N || ld_gy % 8 != 0) return fail(QUEST_EINVAL, "ld_gy must be >= N and a multiple of 8");
+    if (rms_group != 128 && rms_group != K) return fail(QUEST_EINVAL, "rms_group must be 128 or K");
+    if (out_dtype != QUEST_BF16 && out_dtype != QUEST_FP32) return fail(QUEST_EINVAL, "invalid out_dtype");
+    if (accumulate != 0 && accumulate != 1) return fail(QUEST_EINVAL, "accumulate must be 0 or 1");
+    if (accumulate && out_dtype != QUEST_FP32) return fail(QUEST_EINVAL, "accumulate needs an fp32 gradient");
+    const int cb = code_bits(bits, code_mode);
+    if (N > 0 && K > 0) {
+        if (N > (int64_t(1) << 44) / K) return fail(QUEST_EINVAL, "N * K must be <= 2^44");
+        if (!grad_w) return fail(QUEST_EINVAL, "grad_w must be non-NULL");
+        if (T > 0 && (!grad_y || !codes || !scales)) return fail(QUEST_EINVAL, "grad_y, codes and scales must be non-NULL");
+        if (!aligned(grad_w, 16) || !aligned(mask, 16) || (T > 0 && (!aligned(grad_y, 16) || !aligned(codes, 16))))
+            return fail(QUEST_EINVAL, "grad_y, codes, mask and grad_w must be 16-byte aligned");
+        if (T > 0 && !aligned(scales, 4)) return fail(QUEST_EINVAL, "scales must be 4-byte aligned");
+        const int64_t gw_n = N * K * (out_dtype == QUEST_BF16 ? 2 : 4);
+        const void* in[4] = {grad_y, codes, scales, mask};
+        const int64_t in_n[4] = {T > 0 ? ((T - 1) * ld_gy + N) * 2 : 0, T * K * cb / 8, T * (K / rms_group) * 4, N * K / 8};
+        for (int j = 0; j < 4; ++j)
+            if (overlap(grad_w, gw_n, in[j], in_n[j])) return fail(QUEST_EINVAL, "grad_w must not overlap the inputs");
+        const size_t need = weight_grad_workspace_bytes(T, N, K);
+        if (need > 0) {
+            if (!workspace || workspace_bytes < need)
+                return fail(QUEST_EINVAL, "workspace must hold quest_weight_grad_workspace(T, N, K) bytes");
+            if (!aligned(workspace, 16)) return fail(QUEST_EINVAL, "workspace must be 16-byte aligned");
+            for (int j = 0; j < 4; ++j)
+                if (overlap(workspace, (int64_t)need, in[j], in_n[j]))
+                    return fail(QUEST_EINVAL, "workspace must not overlap the inputs");
+            if (overlap(workspace, (int64_t)need, grad_w, gw_n))
+                return fail(QUEST_EINVAL, "workspace must not overlap grad_w");
+        }
+    }
+    if (take_fault(QUEST_FAULT_LAUNCH)) return injected_launch_failure("quest_weight_grad");
+    const bool operand = code_mode == QUEST_CODES_GEMM_OPERAND || code_mode == QUEST_CODES_FP4_OPERAND;
+    WeightGradArgs a = {};
+    a.gy = static_cast<const uint16_t*>(grad_y);
+    a.ld_gy = ld_gy;
+    a.codes = static_cast<const uint8_t*>(codes);
+    a.code_bits = cb;
+    a.offset = operand ? 128.0f : (cb == 8 ? 127.5f : 7.5f);   // c + 128; q + 128 - 1/2; q + 8 - 1/2
+    a.mul = operand ? 0.5f : 1.0f;
+    a.scales = scales;
+    a.groups = K > 0 ? K / rms_group : 1;
+    a.mask = static_cast<const uint8_t*>(mask);
+    a.T = T; a.N = N; a.K = K;
+    a.out = grad_w;
+    a.out_fp32 = out_dtype == QUEST_FP32;
+    a.accumulate = accumulate;
+    a.workspace = workspace;
+    cudaError_t e = launch_weight_grad(a, static_cast<cudaStream_t>(stream));
+    if (e == cudaErrorInvalidValue) return fail(QUEST_ECUDA, "quest_weight_grad: tensor map encoding failed");
+    if (e != cudaSuccess) return cuda_fail(e, "quest_weight_grad launch");
+    return QUEST_OK;
+}
+
+}  // extern "C"
+
+// Shared by the two low-bit calls (up_codes null with `gated` false).
+static quest_status lowbit(const char* what, bool gated, const void* x, int64_t ld_x, const void* const (&codes)[2],
+                           const float* const (&scales)[2], quest_code_mode code_mode, int64_t rms_group, int64_t M,
+                           int64_t N, int64_t K, int had_block, quest_act act, void* y, void* stream) {
+    g_last_error.clear();
+    if (M < 0 || N < 0 || K < 0) return fail(QUEST_EINVAL, "M, N (F) and K must be >= 0");
+    if (N > kMaxDim) return fail(QUEST_EINVAL, "N (F) must be < 2^31");
+    if (M > 64) return fail(QUEST_EUNSUPPORTED, std::string(what) + ": M must be <= 64");
+    if (K > 32768) return fail(QUEST_EUNSUPPORTED, std::string(what) + ": K must be <= 32768");
+    if (code_mode < QUEST_CODES_PACKED || code_mode > QUEST_CODES_FP4_OPERAND) return fail(QUEST_EINVAL, "invalid code_mode");
+    if (code_mode != QUEST_CODES_PACKED && code_mode != QUEST_CODES_FP4_PACKED)
+        return fail(QUEST_EUNSUPPORTED, std::string(what) + ": codes must be 4-bit packed or packed E2M1");
+    if (had_block != 0 && !valid_had(had_block)) return fail(QUEST_EINVAL, "had_block must be 0, 16, 32, 64, 128 or 256");
+    if (K % 128 != 0 || (had_block == 256 && K % 256 != 0))
+        return fail(QUEST_EINVAL, "K must be a multiple of 128 and of had_block");
+    if (N % 8 != 0) return fail(QUEST_EINVAL, "N (F) must be a multiple of 8");
+    if (ld_x < K || ld_x % 8 != 0) return fail(QUEST_EINVAL, "ld_x must be >= K and a multiple of 8");
+    if (rms_group != 128 && rms_group != K) return fail(QUEST_EINVAL, "rms_group must be 128 or K");
+    if (gated && !valid_act(act)) return fail(QUEST_EINVAL, "invalid act");
+    if (M > 0 && N > 0) {
+        if (!y) return fail(QUEST_EINVAL, "the output must be non-NULL");
+        if (!aligned(y, 16)) return fail(QUEST_EINVAL, "the output must be 16-byte aligned");
+        if (K > 0) {
+            if (!x || !aligned(x, 16)) return fail(QUEST_EINVAL, "x must be non-NULL and 16-byte aligned");
+            if (overlap(y, M * N * 2, x, ((M - 1) * ld_x + K) * 2)) return fail(QUEST_EINVAL, "the output must not overlap x");
+            for (int w = 0; w < (gated ? 2 : 1); ++w) {
+                if (!codes[w] || !scales[w]) return fail(QUEST_EINVAL, "codes and scales must be non-NULL");
+                if (!aligned(codes[w], 16) || !aligned(scales[w], 4))
+                    return fail(QUEST_EINVAL, "codes must be 16-byte and scales 4-byte aligned");
+                if (overlap(y, M * N * 2, codes[w], N * (K / 2)) || overlap(y, M * N * 2, scales[w], N * (K / rms_group) * 4))
+                    return fail(QUEST_EINVAL, "the output must not overlap the codes or scales");
+            }
+        }
+    }
+    if (take_fault(QUEST_FAULT_LAUNCH)) return injected_launch_failure(what);
+    LowbitArgs a = {};
+    a.x = static_cast<const uint16_t*>(x);
+    a.ld_x = ld_x;
+    for (int w = 0; w < (gated ? 2 : 1); ++w) {
+        a.codes[w] = static_cast<const uint8_t*>(codes[w]);
+        a.scales[w] = scales[w];
+    }
+    a.scale_groups = K > 0 ? (int)(K / rms_group) : 1;
+    a.M = M; a.N = N; a.K = K;
+    a.had = had_block;
+    a.fp4 = code_mode == QUEST_CODES_FP4_PACKED;
+    a.act = (int)act;
+    a.y = static_cast<uint16_t*>(y);
+    cudaError_t e = launch_lowbit(a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, (std::string(what) + " launch").c_str());
+    return QUEST_OK;
+}
+
+extern "C" {
+
+quest_status quest_lowbit_linear(const void* x, int64_t ld_x, const void* w_codes, quest_code_mode code_mode,
+                                 const float* w_scales, int64_t rms_group, int64_t M, int64_t N, int64_t K,
+                                 int had_block, void* y, void* stream) {
+    const void* const codes[2] = {w_codes, nullptr};
+    const float* const scales[2] = {w_scales, nullptr};
+    return lowbit("quest_lowbit_linear", false, x, ld_x, codes, scales, code_mode, rms_group, M, N, K, had_block,
+                  QUEST_ACT_SILU, y, stream);
+}
+
+quest_status quest_lowbit_gated(const void* x, int64_t ld_x, const void* gate_codes, const float* gate_scales,
+                                const void* up_codes, const float* up_scales, quest_code_mode code_mode,
+                                int64_t rms_group, int64_t M, int64_t F, int64_t K, int had_block, quest_act act,
+                                void* h, void* stream) {
+    const void* const codes[2] = {gate_codes, up_codes};
+    const float* const scales[2] = {gate_scales, up_scales};
+    return lowbit("quest_lowbit_gated", true, x, ld_x, codes, scales, code_mode, rms_group, M, F, K, had_block, act, h,
+                  stream);
+}
+
 quest_status quest_debug_inject_fault(quest_fault fault) {
     g_last_error.clear();
     if (fault != QUEST_FAULT_NONE && fault != QUEST_FAULT_LAUNCH && fault != QUEST_FAULT_WAIT_TIMEOUT)
@@ -829,12 +1057,18 @@ quest_status quest_device_status(void* stream) {
     if (e != cudaSuccess) return cuda_fail(e, "quest_device_status");
     const int vsp = read_and_clear_sparse_status(s, &e);
     if (e != cudaSuccess) return cuda_fail(e, "quest_device_status");
+    const int vga = read_and_clear_gated_status(s, &e);
+    if (e != cudaSuccess) return cuda_fail(e, "quest_device_status");
+    const int vwg = read_and_clear_weight_grad_status(s, &e);
+    if (e != cudaSuccess) return cuda_fail(e, "quest_device_status");
     if (vg != 0) return fail((quest_status)vg, "a bounded device-side wait in quest_w4a4_linear gave up");
     if (vgr != 0) return fail((quest_status)vgr, "a bounded device-side wait in quest_w4a4_linear_grouped gave up");
     if (vtl != 0)
         return fail((quest_status)vtl, "a bounded device-side wait in quest_trust_bwd_linear or quest_linear_bf16 gave up");
     if (vf4 != 0) return fail((quest_status)vf4, "a bounded device-side wait in quest_fp4_linear gave up");
     if (vsp != 0) return fail((quest_status)vsp, "a bounded device-side wait in quest_w4a4_linear_sparse24 gave up");
+    if (vga != 0) return fail((quest_status)vga, "a bounded device-side wait in quest_gated_linear gave up");
+    if (vwg != 0) return fail((quest_status)vwg, "a bounded device-side wait in quest_weight_grad gave up");
     return QUEST_OK;
 }
 

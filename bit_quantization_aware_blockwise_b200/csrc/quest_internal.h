@@ -133,6 +133,62 @@ cudaError_t launch_w4a4_grouped(const int8_t* A, const float* sa, const int8_t* 
                                 int64_t M, int64_t N, int64_t K, uint16_t* y, float* y32,
                                 cudaStream_t stream);
 
+// Gated feed-forward block (gated_linear.cu, gated_bwd.cu): h = act(x wg^T) (x wu^T) with an optional 8-bit
+// checkpoint of both projections, and the backward from it.
+struct GatedArgs {
+    const uint16_t *x, *wg, *wu;   // bf16 [M, K], [F, K], [F, K]
+    int64_t M, F, K;
+    int act;
+    uint16_t* h;                   // bf16 [M, F]
+    int8_t* codes;                 // [M, 2F], or null
+    float* scales;                 // [M, 2 ceil(F / 128)]
+};
+cudaError_t launch_gated_linear(const GatedArgs& a, cudaStream_t stream);
+int read_and_clear_gated_status(cudaStream_t stream, cudaError_t* err);
+
+struct GatedBwdArgs {
+    const uint16_t* gh;            // bf16 [M, F]
+    const int8_t* codes;
+    const float* scales;
+    int64_t M, F;
+    int act;
+    uint16_t *grad, *h;            // bf16 [M, 2F]; [M, F] or null
+};
+cudaError_t launch_gated_bwd(const GatedBwdArgs& a, cudaStream_t stream);
+
+// Weight gradient from the saved codes of the input (weight_grad.cu).
+struct WeightGradArgs {
+    const uint16_t* gy;            // bf16 [T, ld_gy]
+    int64_t ld_gy;
+    const uint8_t* codes;          // [T, K * code_bits / 8]
+    int code_bits;                 // 8 or 4
+    float offset, mul;             // value = ((field as unsigned) - offset) * (step * mul)
+    const float* scales;           // [T, groups]
+    int64_t groups;
+    const uint8_t* mask;           // [N, K / 8] or null
+    int64_t T, N, K;
+    void* out;                     // [N, K]
+    int out_fp32, accumulate;
+    void* workspace;
+};
+size_t weight_grad_workspace_bytes(int64_t T, int64_t N, int64_t K);
+cudaError_t launch_weight_grad(const WeightGradArgs& a, cudaStream_t stream);
+int read_and_clear_weight_grad_status(cudaStream_t stream, cudaError_t* err);
+
+// Few tokens on 4-bit weight codes (lowbit_linear.cu); codes[1] null: the plain layer, else the gated block.
+struct LowbitArgs {
+    const uint16_t* x;             // bf16 [M, ld_x]
+    int64_t ld_x;
+    const uint8_t* codes[2];       // [N, K / 2]
+    const float* scales[2];        // [N, scale_groups]
+    int scale_groups;
+    int64_t M, N, K;
+    int had;                       // 0, 16 .. 256
+    int fp4, act;
+    uint16_t* y;                   // bf16 [M, N]
+};
+cudaError_t launch_lowbit(const LowbitArgs& a, cudaStream_t stream);
+
 // Number of SMs and max resident CTAs of `func` per SM on the current device.
 int sm_count();
 int max_ctas_per_sm(const void* func, int threads, size_t smem);

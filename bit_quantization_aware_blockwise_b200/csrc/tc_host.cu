@@ -61,9 +61,9 @@ bool make_map_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uin
 // Co-resident CTA pairs of a cluster kernel on the current device (cached per
 // kernel; the kernel's shared-memory attribute must already be set).
 int pair_clusters(int dev, const void* kernel, int threads, uint32_t smem) {
-    constexpr int kSlots = 4;
-    static int cached_dev[kSlots] = {-1, -1, -1, -1}, cached[kSlots] = {0, 0, 0, 0};
-    static const void* cached_fn[kSlots] = {nullptr, nullptr, nullptr, nullptr};
+    constexpr int kSlots = 32;   // more than the library's pair kernels
+    static int cached_dev[kSlots] = {}, cached[kSlots] = {};
+    static const void* cached_fn[kSlots] = {};
     static int next_slot = 0;
     static std::mutex mu;
     std::lock_guard<std::mutex> lock(mu);

@@ -1,0 +1,710 @@
+// Weight gradient of the quantized linear layer from the saved codes of its input,
+// with the trust backward fused into the epilogue.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace quest {
+namespace {
+// Device-side status word of this file's kernels (0 = fine). Written only when a
+// bounded wait gives up; read and cleared by quest_device_status().
+__device__ int g_tc_status = 0;
+}  // namespace
+}  // namespace quest
+
+#include "tc_common.cuh"
+
+namespace quest {
+namespace {
+
+// ---------------------------------------------------------------------------
+//   G[n][k]  = sum_t gy[t][n] xh[t][k],  xh[t][k] = bf16((q[t][k] + 1/2) Delta[t][group of k])
+//   gw[n][b] = H (mask[n][b] * G[n][b]) / sqrt(128)   per 128-column block b of a row
+//
+// The reduction runs over the tokens, the outer dimension of both operands, so the MMA
+// takes both transposed (MN-major): a stage row is one token's 64 columns (128 bytes,
+// 128-byte swizzle), which is how gy [T, N] and the codes [T, K] lie in memory. Nothing
+// is transposed or dequantised in HBM.
+//
+// CTA pairs, M = 256 rows of G, N = 256 columns, K = 16 tokens per MMA, 64 tokens per stage.
+// Roles per CTA: one warp loads gy tiles by TMA, one loads the raw codes by TMA into a ring of their own, four
+// warps turn codes into the bf16 B tile (byte -> fp32 by a byte permute onto 2^15, minus the
+// offset, times the token's step, rounded to bf16 as the quantizer's dequant is), one
+// thread of the even CTA issues the MMAs, four warps run the epilogue.
+constexpr int kWThreads = 352;
+constexpr int kConvWarps = 4;
+constexpr int kTokens = 64;                                // tokens per stage
+constexpr uint32_t kWBox = kTokens * 128;                  // one 64-column box: 64 rows of 128 bytes
+constexpr int kWStages = 5;
+constexpr int kRawStages = 5;
+constexpr uint32_t kWStageA = 2 * kWBox, kWStageB = 2 * kWBox;
+constexpr uint32_t kRawBytes = kTokens * 128;              // 8-bit codes of 128 columns (half of it for 4 bits)
+constexpr uint32_t kWChunk = BM * 64;                      // epilogue staging: 128 rows of 64 bytes
+constexpr uint32_t kWSmemA = 0;
+constexpr uint32_t kWSmemB = kWSmemA + kWStages * kWStageA;
+constexpr uint32_t kWSmemRaw = kWSmemB + kWStages * kWStageB;
+constexpr uint32_t kWSmemC = kWSmemRaw + kRawStages * kRawBytes;
+constexpr uint32_t kWSmemBar = kWSmemC + 2 * kWChunk;
+constexpr uint32_t kWNumBars = 3 * kWStages + 2 * kRawStages + 4 + 1;
+constexpr uint32_t kWSmemTmemSlot = kWSmemBar + kWNumBars * 8;
+constexpr uint32_t kWSmemAbort = kWSmemTmemSlot + 4;
+constexpr uint32_t kWSmemTotal = kWSmemAbort + 4 + 1024;
+static_assert(kWSmemTotal <= 227 * 1024, "weight gradient shared memory");
+
+constexpr uint32_t kIdescBf16Mn = (1u << 4)      // D: fp32
+                                | (1u << 7)      // A: bf16
+                                | (1u << 10)     // B: bf16
+                                | (1u << 15)     // A transposed (MN-major)
+                                | (1u << 16)     // B transposed (MN-major)
+                                | (uint32_t(BN >> 3) << 17) | (uint32_t(256 >> 4) << 24);
+
+// MN-major tile of 64-column boxes with 128-byte rows, one row per token, 128-byte
+// swizzle: boxes kWBox apart along M / N, groups of 8 tokens 1024 bytes apart along K.
+__device__ __forceinline__ uint64_t smem_desc_mn128(uint32_t addr) {
+    uint64_t d = 0;
+    d |= uint64_t((addr >> 4) & 0x3FFFu);
+    d |= uint64_t(kWBox >> 4) << 16;
+    d |= uint64_t(1024 >> 4) << 32;
+    d |= uint64_t(1) << 46;                        // descriptor version (sm_100)
+    d |= uint64_t(2) << 61;                        // layout: 128-byte swizzle
+    return d;
+}
+
+__device__ __forceinline__ void tc_mma_bf16_mn_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                                    uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(kIdescBf16Mn), "r"(accumulate)
+        : "memory");
+}
+
+// Arrival on the even CTA's barrier that publishes this warp's tile stores (already fenced
+// for the async proxy) to the MMA issuer, and the issuer's matching wait: cluster scope, since
+// the writers may be in the odd CTA.
+__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(kSuspendMmaNs)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait_cluster(bar, parity)) return true;
+        if ((it & 63u) == 0) {
+            if (*abort_flag) return false;
+            if (global_timer_ns() - t0 > kWaitLimitNs) {
+                *abort_flag = 1;
+                atomicExch(&g_tc_status, (int)QUEST_ETIMEOUT);
+                return false;
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ void tma_reduce_add_2d(const CUtensorMap* map, uint32_t src, int c0, int c1) {
+    asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(src)
+                 : "memory");
+}
+
+struct WeightGradParams {
+    const uint8_t* mask;        // trust mask bits of the weight [N, K / 8], or null (all kept)
+    const float* scales;        // [T, groups]
+    int64_t scale_stride;       // groups: 1 (a step per token) or K / 128
+    float offset;               // code byte as unsigned -> value: (2^15 + u) - offset, times step * mul
+    float mul;
+    uint32_t flip;              // makes the stored two's complement fields unsigned
+    int T, N, K;
+    int num_n, num_k;           // 256-row and 256-column tiles of G
+    int splits, blocks_per_split, num_tb;   // token blocks of 64: in all, and per split
+    int raw_rows;               // rows of one split's slice of the workspace
+    int add;                    // fp32 output: added to what is there
+};
+
+enum { kOutBf16 = 0, kOutF32 = 1, kOutRaw = 2 };
+
+// Unnormalised 128-point Walsh-Hadamard transform (Sylvester order) of one thread's registers.
+__device__ __forceinline__ void fwht128(float2 (&w)[64]) {
+#pragma unroll
+    for (int j = 0; j < 64; ++j) w[j] = make_float2(w[j].x + w[j].y, w[j].x - w[j].y);
+#pragma unroll
+    for (int h = 1; h < 64; h <<= 1) {
+#pragma unroll
+        for (int j = 0; j < 64; ++j) {
+            if ((j & h) == 0) {
+                const float2 a = w[j], b = w[j + h];
+                w[j] = __fadd2_rn(a, b);
+                w[j + h] = __ffma2_rn(b, make_float2(-1.0f, -1.0f), a);
+            }
+        }
+    }
+}
+
+constexpr float kInvSqrt128 = 0.08838834764831845f;
+
+// Four unsigned code bytes -> four bf16 values (two words).
+__device__ __forceinline__ void convert4(uint32_t u, float2 neg_off, float2 step, uint32_t& lo, uint32_t& hi) {
+    // 0x4700uu00 is 2^15 + uu
+    const float2 a = make_float2(__uint_as_float(__byte_perm(u, 0x47000000u, 0x7404)),
+                                 __uint_as_float(__byte_perm(u, 0x47000000u, 0x7414)));
+    const float2 b = make_float2(__uint_as_float(__byte_perm(u, 0x47000000u, 0x7424)),
+                                 __uint_as_float(__byte_perm(u, 0x47000000u, 0x7434)));
+    const float2 va = __fmul2_rn(__fadd2_rn(a, neg_off), step), vb = __fmul2_rn(__fadd2_rn(b, neg_off), step);
+    const __nv_bfloat162 ha = __floats2bfloat162_rn(va.x, va.y), hb = __floats2bfloat162_rn(vb.x, vb.y);
+    lo = *reinterpret_cast<const uint32_t*>(&ha);
+    hi = *reinterpret_cast<const uint32_t*>(&hb);
+}
+
+// CB: bits of a stored code (8 or 4). OUT: kOutBf16 / kOutF32 finish the gradient; kOutRaw
+// stores the plain sums of one token split for weight_grad_finish_kernel.
+template <int CB, int OUT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWThreads, 1)
+weight_grad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_constant__ CUtensorMap map_q,
+                   const __grid_constant__ CUtensorMap map_o, const WeightGradParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t bar_fulla = sbase + kWSmemBar;                // [kWStages] gy landed (even CTA)
+    const uint32_t bar_fullb = bar_fulla + 8 * kWStages;         // [kWStages] B tile converted (even CTA)
+    const uint32_t bar_empty = bar_fullb + 8 * kWStages;         // [kWStages] MMAs done with the stage
+    const uint32_t bar_rfull = bar_empty + 8 * kWStages;         // [kRawStages] raw codes landed
+    const uint32_t bar_rempty = bar_rfull + 8 * kRawStages;      // [kRawStages] raw codes read
+    const uint32_t bar_tfull = bar_rempty + 8 * kRawStages;      // [2]
+    const uint32_t bar_tempty = bar_tfull + 16;                  // [2] (even CTA)
+    const uint32_t bar_drain = bar_tempty + 16;                  // [1]
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kWSmemAbort);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kWSmemTmemSlot);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const bool even = rank == 0;
+    const int pair = blockIdx.x >> 1, num_pairs = gridDim.x >> 1;
+    const int tiles = p.num_n * p.num_k;
+    const int num_items = tiles * p.splits;   // split-major: the pairs in flight share a token range
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kWStages; ++s) {
+            mbar_init(bar_fulla + 8 * s, 1);
+            mbar_init(bar_fullb + 8 * s, 2 * kConvWarps);
+            mbar_init(bar_empty + 8 * s, 1);
+        }
+        for (int s = 0; s < kRawStages; ++s) {
+            mbar_init(bar_rfull + 8 * s, 1);
+            mbar_init(bar_rempty + 8 * s, kConvWarps);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(bar_tfull + 8 * b, 1);
+            mbar_init(bar_tempty + 8 * b, 2);
+        }
+        mbar_init(bar_drain, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    pdl_wait();
+    pdl_trigger();
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ gy producer (both CTAs)
+        if (lane == 0) {
+            const uint32_t full_even = map_to_rank(bar_fulla, 0);
+            uint32_t stage = 0, phase = 0;
+            uint64_t issued = 0;
+            bool ok = true;
+            for (int item = pair; item < num_items && ok; item += num_pairs) {
+                const int tile = item % tiles, split = item / tiles;
+                const int n0 = (tile / p.num_k) * 256 + 128 * int(rank);
+                const int tb0 = split * p.blocks_per_split, tb1 = min(tb0 + p.blocks_per_split, p.num_tb);
+                for (int tb = tb0; tb < tb1; ++tb) {
+                    if (!mbar_wait(bar_empty + 8 * stage, phase ^ 1, abort_flag, kWaitLimitNs, kSuspendProducerNs)) {
+                        ok = false;
+                        break;
+                    }
+                    if (even) mbar_arrive_expect_tx(bar_fulla + 8 * stage, 2 * kWStageA);
+                    const uint32_t fb = full_even + 8 * stage, dst = sbase + kWSmemA + stage * kWStageA;
+                    tma_load_2d_pair(dst, &map_g, n0, tb * kTokens, fb);
+                    tma_load_2d_pair(dst + kWBox, &map_g, n0 + 64, tb * kTokens, fb);
+                    ++issued;
+                    if (++stage == kWStages) { stage = 0; phase ^= 1; }
+                }
+            }
+            // giving up: no CTA may leave while a copy into its shared memory is in flight
+            if (!ok && even) {
+                const uint64_t n = issued < kWStages ? issued : kWStages;
+                for (uint64_t i = issued - n; i < issued; ++i) {
+                    const uint32_t st = uint32_t(i % kWStages), ph = uint32_t((i / kWStages) & 1);
+                    const uint64_t t0 = global_timer_ns();
+                    while (!mbar_try_wait(bar_fulla + 8 * st, ph) && global_timer_ns() - t0 < kWaitLimitNs) {
+                    }
+                }
+            } else if (!ok) {
+                const uint64_t t0 = global_timer_ns();
+                while (global_timer_ns() - t0 < 10000000ull) {
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer (even CTA)
+        if (even && lane == 0) {
+            uint32_t stage = 0, phase = 0;
+            bool ok = true;
+            int local = 0;
+            for (int item = pair; item < num_items && ok; item += num_pairs, ++local) {
+                const int split = item / tiles;
+                const int tb0 = split * p.blocks_per_split, tb1 = min(tb0 + p.blocks_per_split, p.num_tb);
+                const uint32_t buf = local & 1, bphase = (local >> 1) & 1;
+                if (!mbar_wait(bar_tempty + 8 * buf, bphase ^ 1, abort_flag, kWaitLimitNs, kSuspendMmaNs)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + buf * BN;
+                for (int tb = tb0; tb < tb1; ++tb) {
+                    if (!mbar_wait(bar_fulla + 8 * stage, phase, abort_flag, kWaitLimitNs, kSuspendMmaNs) ||
+                        !mbar_wait_cluster(bar_fullb + 8 * stage, phase, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a_addr = sbase + kWSmemA + stage * kWStageA;
+                    const uint32_t b_addr = sbase + kWSmemB + stage * kWStageB;
+#pragma unroll
+                    for (int kk = 0; kk < kTokens / 16; ++kk) {
+                        tc_mma_bf16_mn_pair(d_tmem, smem_desc_mn128(a_addr + kk * 2048),
+                                            smem_desc_mn128(b_addr + kk * 2048), tb != tb0 || kk != 0);
+                    }
+                    tc_commit_pair_mc(bar_empty + 8 * stage);
+                    if (++stage == kWStages) { stage = 0; phase ^= 1; }
+                }
+                if (!ok) break;
+                tc_commit_pair_mc(bar_tfull + 8 * buf);
+            }
+            tc_commit_pair(bar_drain);
+            const uint64_t t0 = global_timer_ns();
+            while (!mbar_try_wait(bar_drain, 0) && global_timer_ns() - t0 < kWaitLimitNs) {
+            }
+        }
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ raw code producer (both CTAs)
+        if (lane == 0) {
+            uint32_t stage = 0, phase = 0;
+            uint64_t issued = 0;
+            bool ok = true;
+            for (int item = pair; item < num_items && ok; item += num_pairs) {
+                const int tile = item % tiles, split = item / tiles;
+                const int k0 = (tile % p.num_k) * BN + 128 * int(rank);
+                const int tb0 = split * p.blocks_per_split, tb1 = min(tb0 + p.blocks_per_split, p.num_tb);
+                for (int tb = tb0; tb < tb1; ++tb) {
+                    if (!mbar_wait(bar_rempty + 8 * stage, phase ^ 1, abort_flag, kWaitLimitNs, kSuspendProducerNs)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(bar_rfull + 8 * stage, kRawBytes * CB / 8);
+                    tma_load_2d(sbase + kWSmemRaw + stage * kRawBytes, &map_q, k0 * CB / 8, tb * kTokens,
+                                bar_rfull + 8 * stage);
+                    ++issued;
+                    if (++stage == kRawStages) { stage = 0; phase ^= 1; }
+                }
+            }
+            if (!ok) {
+                const uint64_t n = issued < kRawStages ? issued : kRawStages;
+                for (uint64_t i = issued - n; i < issued; ++i) {
+                    const uint32_t st = uint32_t(i % kRawStages), ph = uint32_t((i / kRawStages) & 1);
+                    const uint64_t t0 = global_timer_ns();
+                    while (!mbar_try_wait(bar_rfull + 8 * st, ph) && global_timer_ns() - t0 < kWaitLimitNs) {
+                    }
+                }
+            }
+        }
+    } else if (warp < 3 + kConvWarps) {
+        // ------------------------------------------------------------ code conversion (warps 3..6, both CTAs)
+        const int cw = warp - 3;
+        const int t = (cw & 1) * 32 + lane;    // token of the block
+        const int half = cw >> 1;              // 64-column box of the CTA's 128 columns
+        const uint32_t fullb_even = map_to_rank(bar_fullb, 0);
+        const float2 neg_off = make_float2(-p.offset, -p.offset);
+        uint32_t stage = 0, phase = 0, rstage = 0, rphase = 0;
+        bool ok = true;
+        for (int item = pair; item < num_items && ok; item += num_pairs) {
+            const int tile = item % tiles, split = item / tiles;
+            const int k0 = (tile % p.num_k) * BN + 128 * int(rank);
+            const int tb0 = split * p.blocks_per_split, tb1 = min(tb0 + p.blocks_per_split, p.num_tb);
+            // this token's step, fetched one block ahead; 0 past the last token or column, where
+            // the codes read as zero too
+            const float* sc = p.scales + (p.scale_stride == 1 ? 0 : k0 / 128);
+            auto step_of = [&](int tb) {
+                const int64_t tok = int64_t(tb) * kTokens + t;
+                return tok < p.T && k0 < p.K && tb < tb1 ? __ldg(sc + tok * p.scale_stride) * p.mul : 0.0f;
+            };
+            float next = step_of(tb0);
+            for (int tb = tb0; tb < tb1; ++tb) {
+                const float2 step = make_float2(next, next);
+                next = step_of(tb + 1);
+                // (giving up is decided by the whole warp: its lanes meet again below)
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar_rfull + 8 * rstage, rphase, abort_flag, kWaitLimitNs,
+                                                       kSuspendProducerNs))) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t raw = sbase + kWSmemRaw + rstage * kRawBytes;
+                uint4 q[4];
+#pragma unroll
+                for (int j = 0; j < CB / 2; ++j) {
+                    const uint32_t at = CB == 8 ? raw + t * 128 + (((half * 4 + j) ^ (t & 7)) << 4)
+                                                : raw + t * 64 + (((half * 2 + j) ^ ((t >> 1) & 3)) << 4);
+                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                 : "=r"(q[j].x), "=r"(q[j].y), "=r"(q[j].z), "=r"(q[j].w)
+                                 : "r"(at)
+                                 : "memory");
+                }
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar_empty + 8 * stage, phase ^ 1, abort_flag, kWaitLimitNs,
+                                                       kSuspendProducerNs))) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t row = sbase + kWSmemB + stage * kWStageB + half * kWBox + t * 128;
+#pragma unroll
+                for (int j = 0; j < CB / 2; ++j) {
+                    const uint32_t w[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
+                    if constexpr (CB == 8) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t o[4];
+                            convert4(w[2 * h] ^ p.flip, neg_off, step, o[0], o[1]);
+                            convert4(w[2 * h + 1] ^ p.flip, neg_off, step, o[2], o[3]);
+                            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
+                                             row + (((2 * j + h) ^ (t & 7)) << 4)),
+                                         "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                                         : "memory");
+                        }
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            // low nibbles are the even elements, high nibbles the odd ones
+                            const uint32_t u = w[h] ^ p.flip, ev = u & 0x0F0F0F0Fu, od = (u >> 4) & 0x0F0F0F0Fu;
+                            uint32_t o[4];
+                            convert4(__byte_perm(ev, od, 0x5140), neg_off, step, o[0], o[1]);
+                            convert4(__byte_perm(ev, od, 0x7362), neg_off, step, o[2], o[3]);
+                            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
+                                             row + (((4 * j + h) ^ (t & 7)) << 4)),
+                                         "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                                         : "memory");
+                        }
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    // the raw slot is returned only now that its values have arrived and been used: an arrival
+                    // right behind the loads does not wait for them, and rarely let the next copy overtake one
+                    mbar_arrive(bar_rempty + 8 * rstage);
+                    mbar_arrive_release_cluster(fullb_even + 8 * stage);
+                }
+                if (++rstage == kRawStages) { rstage = 0; rphase ^= 1; }
+                if (++stage == kWStages) { stage = 0; phase ^= 1; }
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ epilogue (warps 7..10, both CTAs)
+        const int et = threadIdx.x - 32 * (3 + kConvWarps);
+        const int quarter = warp & 3;
+        const int row_in_tile = quarter * 32 + lane;
+        const uint32_t lane_addr = uint32_t(quarter * 32) << 16;
+        const uint32_t tempty_even = map_to_rank(bar_tempty, 0);
+        int local = 0;
+        int cbuf = 0;
+        for (int item = pair; item < num_items; item += num_pairs, ++local) {
+            const int tile = item % tiles, split = item / tiles;
+            const int n0 = (tile / p.num_k) * 256 + 128 * int(rank), k0 = (tile % p.num_k) * BN;
+            const uint32_t buf = local & 1, bphase = (local >> 1) & 1;
+            const int n = n0 + row_in_tile;
+            uint4 mw[2] = {make_uint4(~0u, ~0u, ~0u, ~0u), make_uint4(~0u, ~0u, ~0u, ~0u)};
+            if (OUT != kOutRaw && p.mask != nullptr) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const int kb0 = k0 + 128 * b;
+                    if (n < p.N && kb0 < p.K)
+                        mw[b] = *reinterpret_cast<const uint4*>(p.mask + int64_t(n) * (p.K / 8) + kb0 / 8);
+                }
+            }
+            const bool got = mbar_wait(bar_tfull + 8 * buf, bphase, abort_flag, kWaitLimitNs, kSuspendEpilogueNs);
+            if (epi_any(!got)) break;
+            tc_fence_after();
+            const uint32_t t_acc = tmem_base + lane_addr + buf * BN;
+#pragma unroll 1
+            for (int b = 0; b < 2; ++b) {
+                if (n0 >= p.N || k0 + 128 * b >= p.K) break;   // nothing of this block is stored (uniform)
+                const uint4 mb = b == 0 ? mw[0] : mw[1];
+                float2 w[64];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t r[32];
+                    QUEST_TMEM_LD32(t_acc + 128 * b + 32 * c, r);
+                    tmem_wait_ld();
+                    const uint32_t bits = c == 0 ? mb.x : c == 1 ? mb.y : c == 2 ? mb.z : mb.w;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        if constexpr (OUT != kOutRaw) {
+                            const uint32_t k0m = 0u - ((bits >> (2 * i)) & 1u);
+                            const uint32_t k1m = 0u - ((bits >> (2 * i + 1)) & 1u);
+                            w[16 * c + i] =
+                                make_float2(__uint_as_float(r[2 * i] & k0m), __uint_as_float(r[2 * i + 1] & k1m));
+                        } else {
+                            w[16 * c + i] = make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+                        }
+                    }
+                }
+                if constexpr (OUT != kOutRaw) fwht128(w);
+                constexpr int kChunks = OUT == kOutBf16 ? 4 : 8;   // of 64 bytes a row: 32 bf16 or 16 fp32 columns
+                constexpr float kScale = OUT == kOutRaw ? 1.0f : kInvSqrt128;
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) {
+                    const uint32_t stg = sbase + kWSmemC + cbuf * kWChunk + row_in_tile * 64;
+                    const uint32_t swz = (row_in_tile >> 1) & 3;
+#pragma unroll
+                    for (int q16 = 0; q16 < 4; ++q16) {
+                        uint32_t o[4];
+                        if constexpr (OUT == kOutBf16) {
+#pragma unroll
+                            for (int h = 0; h < 4; ++h) {
+                                const float2 v = w[16 * c + 4 * q16 + h];
+                                const __nv_bfloat162 hb = __floats2bfloat162_rn(v.x * kScale, v.y * kScale);
+                                o[h] = *reinterpret_cast<const uint32_t*>(&hb);
+                            }
+                        } else {
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const float2 v = w[8 * c + 2 * q16 + h];
+                                o[2 * h] = __float_as_uint(v.x * kScale);
+                                o[2 * h + 1] = __float_as_uint(v.y * kScale);
+                            }
+                        }
+                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(stg + ((q16 ^ swz) << 4)),
+                                     "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                                     : "memory");
+                    }
+                    fence_proxy_async_smem();
+                    epi_bar();
+                    if (et == 0) {
+                        const int col = k0 + 128 * b + c * (128 / kChunks);
+                        const uint32_t src = sbase + kWSmemC + cbuf * kWChunk;
+                        if (OUT == kOutRaw)
+                            tma_store_2d(&map_o, src, col, split * p.raw_rows + n0);
+                        else if (OUT == kOutF32 && p.add)
+                            tma_reduce_add_2d(&map_o, src, col, n0);
+                        else
+                            tma_store_2d(&map_o, src, col, n0);
+                        bulk_commit();
+                        bulk_wait_read_le1();
+                    }
+                    epi_bar();
+                    cbuf ^= 1;
+                }
+            }
+            tc_fence_before();
+            epi_bar();
+            if (et == 0) mbar_arrive_remote(tempty_even + 8 * buf);
+        }
+        if (et == 0) bulk_wait_all();
+    }
+
+    tc_fence_before();
+    cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols)
+                     : "memory");
+    }
+}
+
+// Sum of the token splits' plain sums in split order, mask, transform, store: a warp per
+// 128-column block of a row, four columns a lane.
+template <typename Out>
+__global__ void __launch_bounds__(256) weight_grad_finish_kernel(const float4* __restrict__ part, const uint8_t* mask,
+                                                                 Out* out, int64_t n_rows, int K, int splits,
+                                                                 int64_t raw_rows, int add) {
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const int64_t kblocks = K / 128, total = n_rows * kblocks;
+    for (int64_t i = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; i < total;
+         i += (int64_t(gridDim.x) * blockDim.x) >> 5) {
+        const int64_t n = i / kblocks, kb = i % kblocks;
+        float4 v = part[(n * K + kb * 128) / 4 + lane];
+        for (int s = 1; s < splits; ++s) {
+            const float4 u = part[((s * raw_rows + n) * K + kb * 128) / 4 + lane];
+            v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+        }
+        if (mask) {
+            const uint32_t bits = mask[n * (K / 8) + kb * 16 + (lane >> 1)] >> (4 * (lane & 1));
+            if (!(bits & 1)) v.x = 0.0f;
+            if (!(bits & 2)) v.y = 0.0f;
+            if (!(bits & 4)) v.z = 0.0f;
+            if (!(bits & 8)) v.w = 0.0f;
+        }
+        const float2 a = make_float2(v.x + v.y, v.x - v.y), b = make_float2(v.z + v.w, v.z - v.w);
+        float t[4] = {a.x + b.x, a.y + b.y, a.x - b.x, a.y - b.y};
+#pragma unroll
+        for (int h = 1; h < 32; h <<= 1) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float o = __shfl_xor_sync(0xFFFFFFFFu, t[j], h);
+                t[j] = lane & h ? o - t[j] : t[j] + o;
+            }
+        }
+        Out* dst = out + n * K + kb * 128 + 4 * lane;
+        if constexpr (sizeof(Out) == 4) {
+            float4* d4 = reinterpret_cast<float4*>(dst);
+            float4 r = make_float4(t[0] * kInvSqrt128, t[1] * kInvSqrt128, t[2] * kInvSqrt128, t[3] * kInvSqrt128);
+            if (add) {
+                const float4 o = *d4;
+                r.x += o.x; r.y += o.y; r.z += o.z; r.w += o.w;
+            }
+            *d4 = r;
+        } else {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(t[0] * kInvSqrt128, t[1] * kInvSqrt128);
+            const __nv_bfloat162 hi = __floats2bfloat162_rn(t[2] * kInvSqrt128, t[3] * kInvSqrt128);
+            *reinterpret_cast<uint2*>(dst) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+        }
+    }
+}
+
+// Token splits: with fewer output tiles than CTA pairs, the tokens are cut so that the pairs left idle
+// take part, in pieces of at least kMinBlocks blocks of 64 tokens (a piece costs its partial's
+// round trip through the workspace, 256 KB a tile, worth about that many blocks of MMAs).
+constexpr int kMinBlocks = 8;
+
+struct SplitPlan {
+    int splits, blocks_per_split, num_tb;
+    int64_t raw_rows;
+};
+
+SplitPlan plan_splits(int64_t T, int64_t N, int64_t K) {
+    SplitPlan s;
+    s.num_tb = (int)((T + kTokens - 1) / kTokens);
+    s.raw_rows = (N + 255) / 256 * 256;
+    const int64_t tiles = ((N + 255) / 256) * ((K + BN - 1) / BN);
+    const int64_t pairs = sm_count() / 2;
+    int64_t want = tiles >= pairs || tiles == 0 ? 1 : pairs / tiles;
+    const int64_t most = s.num_tb / kMinBlocks > 1 ? s.num_tb / kMinBlocks : 1;
+    if (want > most) want = most;
+    s.blocks_per_split = s.num_tb > 0 ? (int)((s.num_tb + want - 1) / want) : 1;
+    s.splits = s.num_tb > 0 ? (s.num_tb + s.blocks_per_split - 1) / s.blocks_per_split : 1;
+    return s;
+}
+
+template <int CB, int OUT>
+cudaError_t launch_main(const WeightGradArgs& a, const SplitPlan& plan, cudaStream_t stream) {
+    CUtensorMap mg, mq, mo;
+    void* dst = OUT == kOutRaw ? a.workspace : a.out;
+    const uint64_t rows = OUT == kOutRaw ? uint64_t(plan.splits) * plan.raw_rows : uint64_t(a.N);
+    const bool bf = OUT == kOutBf16;
+    if (!make_map_2d(&mg, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.gy, a.N, a.T, a.ld_gy * 2, 64, kTokens,
+                     CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_map_2d(&mq, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.codes, a.K * CB / 8, a.T, a.K * CB / 8, 128 * CB / 8, kTokens,
+                     CB == 8 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !make_map_2d(&mo, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dst, a.K, rows,
+                     a.K * (bf ? 2 : 4), bf ? 32 : 16, 128, CU_TENSOR_MAP_SWIZZLE_64B))
+        return cudaErrorInvalidValue;
+    WeightGradParams p;
+    p.mask = a.mask;
+    p.scales = a.scales;
+    p.scale_stride = a.groups;
+    p.offset = 32768.0f + a.offset;
+    p.mul = a.mul;
+    p.flip = CB == 8 ? 0x80808080u : 0x88888888u;
+    p.T = (int)a.T; p.N = (int)a.N; p.K = (int)a.K;
+    p.num_n = (int)((a.N + 255) / 256);
+    p.num_k = (int)((a.K + BN - 1) / BN);
+    p.splits = plan.splits;
+    p.blocks_per_split = plan.blocks_per_split;
+    p.num_tb = plan.num_tb;
+    p.raw_rows = (int)plan.raw_rows;
+    p.add = a.accumulate;
+    static thread_local int attr_dev = -1;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (attr_dev != dev) {
+        cudaError_t e = cudaFuncSetAttribute(weight_grad_kernel<CB, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             kWSmemTotal);
+        if (e != cudaSuccess) return e;
+        attr_dev = dev;
+    }
+    const int64_t items = int64_t(p.num_n) * p.num_k * p.splits;
+    const int pairs = pair_clusters(dev, (const void*)weight_grad_kernel<CB, OUT>, kWThreads, kWSmemTotal);
+    const int grid_pairs = items < pairs ? (int)items : pairs;
+    return launch_pdl(weight_grad_kernel<CB, OUT>, dim3(2 * grid_pairs), dim3(kWThreads), kWSmemTotal, stream, mg, mq,
+                      mo, p);
+}
+
+template <int CB>
+cudaError_t launch_bits(const WeightGradArgs& a, const SplitPlan& plan, cudaStream_t stream) {
+    if (plan.splits == 1)
+        return a.out_fp32 ? launch_main<CB, kOutF32>(a, plan, stream) : launch_main<CB, kOutBf16>(a, plan, stream);
+    cudaError_t e = launch_main<CB, kOutRaw>(a, plan, stream);
+    if (e != cudaSuccess) return e;
+    const int64_t blocks = (a.N * (a.K / 128) + 7) / 8;
+    const dim3 grid((unsigned)(blocks < 16384 ? blocks : 16384));
+    const float4* part = static_cast<const float4*>(a.workspace);
+    if (a.out_fp32)
+        return launch_pdl(weight_grad_finish_kernel<float>, grid, dim3(256), 0, stream, part, a.mask,
+                          static_cast<float*>(a.out), a.N, (int)a.K, plan.splits, plan.raw_rows, a.accumulate);
+    return launch_pdl(weight_grad_finish_kernel<uint16_t>, grid, dim3(256), 0, stream, part, a.mask,
+                      static_cast<uint16_t*>(a.out), a.N, (int)a.K, plan.splits, plan.raw_rows, 0);
+}
+
+}  // namespace
+
+size_t weight_grad_workspace_bytes(int64_t T, int64_t N, int64_t K) {
+    if (T == 0 || N == 0 || K == 0) return 0;
+    const SplitPlan s = plan_splits(T, N, K);
+    return s.splits == 1 ? 0 : size_t(s.splits) * size_t(s.raw_rows) * size_t(K) * 4;
+}
+
+cudaError_t launch_weight_grad(const WeightGradArgs& a, cudaStream_t stream) {
+    if (a.N == 0 || a.K == 0) return cudaSuccess;
+    if (a.T == 0) {   // the empty sum: zero, or nothing to add
+        if (a.out_fp32 && a.accumulate) return cudaSuccess;
+        const int64_t halves = a.N * a.K * (a.out_fp32 ? 2 : 1);
+        return launch_zero_fill(static_cast<uint16_t*>(a.out), nullptr, halves, stream);
+    }
+    const SplitPlan plan = plan_splits(a.T, a.N, a.K);
+    return a.code_bits == 8 ? launch_bits<8>(a, plan, stream) : launch_bits<4>(a, plan, stream);
+}
+
+int read_and_clear_weight_grad_status(cudaStream_t stream, cudaError_t* err) {
+    int v = 0, zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_tc_status, sizeof(int), 0, cudaMemcpyDeviceToHost, stream);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+    if (e == cudaSuccess && v != 0)
+        e = cudaMemcpyToSymbolAsync(g_tc_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, stream);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+    *err = e;
+    return v;
+}
+
+}  // namespace quest

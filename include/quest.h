@@ -102,6 +102,14 @@ typedef enum quest_mask_mode {
     QUEST_MASK_BYTES = 1
 } quest_mask_mode;
 
+/* Gate activation of the feed-forward block, act(a) = a sigmoid(z(a)).
+ *   QUEST_ACT_SILU        z = a
+ *   QUEST_ACT_GELU_TANH   z = 2 sqrt(2/pi) (a + 0.044715 a^3), the tanh form of GELU */
+typedef enum quest_act {
+    QUEST_ACT_SILU = 0,
+    QUEST_ACT_GELU_TANH = 1
+} quest_act;
+
 /*
  * quest_quantize_fwd -- QuEST forward quantizer with trust mask.
  *
@@ -428,12 +436,147 @@ quest_status quest_linear_bf16(const void* x_hat, const void* w_hat, int64_t M, 
 quest_status quest_transpose_bf16(const void* src, int64_t rows, int64_t cols, void* dst, void* stream);
 
 /*
+ * quest_gated_linear -- the gated feed-forward block on dequantised operands, forward:
+ * both projections, the activation and the product in one kernel.
+ *
+ * The Llama-style block the pages train (pith.science review, reference excerpts: a
+ * SiLU-gated MLP) up to its down projection, on the operands quest_linear_bf16 takes:
+ *     a = x_hat w_gate^T,  b = x_hat w_up^T       (fp32 accumulation, not rounded)
+ *     h = act(a) * b                              bf16 (RNE)
+ * For training it can keep a and b as an 8-bit checkpoint, the input of quest_gated_bwd.
+ * Per row and group of 128 consecutive columns (the last group of a row may be shorter),
+ * of each projection:
+ *     Delta = max|v| / 128,  q = floor(v / Delta) in [-128, 127],  restored (q + 1/2) Delta,
+ * the midrise form of the quantizer's codes without a clip: no value is off by more than
+ * Delta / 2 (and Delta 2^-22 for a value next to a boundary). A group whose largest magnitude is below
+ * 2^-100 is kept as zeros; a group that holds an Inf or a NaN is restored to non-finite
+ * values throughout.
+ *
+ * Arguments
+ *   x_hat    device bf16 [M, K].   w_gate, w_up   device bf16 [F, K].
+ *   M, F, K  >= 0; F a multiple of 16, K a multiple of 8; each < 2^31. K == 0 gives h = 0.
+ *   act      the activation.
+ *   h        device bf16 [M, F].
+ *   ckpt_codes, ckpt_scales   device int8 [M, 2 F] (a's codes, then b's) and fp32
+ *            [M, 2 ceil(F / 128)] (a's steps, then b's); both given, or both NULL (nothing kept).
+ * All pointers 16-byte aligned (ckpt_scales 4-byte); outputs overlap nothing.
+ * Returns QUEST_OK, QUEST_EINVAL or QUEST_ECUDA; a bounded wait that gives up is reported
+ * by quest_device_status as QUEST_ETIMEOUT.
+ */
+quest_status quest_gated_linear(const void* x_hat, const void* w_gate, const void* w_up, int64_t M, int64_t F,
+                                int64_t K, quest_act act, void* h, int8_t* ckpt_codes, float* ckpt_scales,
+                                void* stream);
+
+/*
+ * quest_gated_bwd -- backward of the block's activation and product from the 8-bit
+ * checkpoint. With a, b restored from their codes and s = sigmoid(z(a)):
+ *     grad_a = grad_h b (s + a s (1 - s) z'(a)),   grad_b = grad_h a s
+ *     h      = a s b                                              (optional)
+ * in fp32, rounded once to bf16. The two gradients are the halves of one [M, 2 F] matrix, so
+ * that the block's input gradient is one quest_trust_bwd_linear (N = 2 F, with the two
+ * transposed weights side by side) and its weight gradient one quest_weight_grad.
+ *
+ * Arguments
+ *   grad_h   device bf16 [M, F].   ckpt_codes, ckpt_scales   as quest_gated_linear wrote them.
+ *   M, F     >= 0; F a multiple of 16; each < 2^31.   act as in the forward.
+ *   grad_ab  device bf16 [M, 2 F]: grad_a in columns 0..F-1, grad_b after them.
+ *   h        device bf16 [M, F], or NULL: the block's output again, from the restored a and b.
+ * All pointers 16-byte aligned (ckpt_scales 4-byte); outputs overlap nothing.
+ * Returns QUEST_OK, QUEST_EINVAL or QUEST_ECUDA.
+ */
+quest_status quest_gated_bwd(const void* grad_h, const int8_t* ckpt_codes, const float* ckpt_scales, int64_t M,
+                             int64_t F, quest_act act, void* grad_ab, void* h, void* stream);
+
+/*
+ * quest_weight_grad -- weight gradient of a QuEST linear layer from the saved codes of
+ * its input, with the trust backward fused into the product.
+ *
+ * The layer's input need not be kept in bf16 between the passes: its codes (8 or 4 bits a
+ * value) and steps stand for the very operand the forward multiplied,
+ *     x_hat  = bf16( (q + 1/2) Delta )                      (quest_quantize_fwd's dequant)
+ *     G      = grad_y^T x_hat                 [N, K]        (fp32 accumulation)
+ *     grad_w = H (m * G) / sqrt(128) per 128-column block
+ * (pith.science review, "What carries the argument" and Figure 2 caption, as for
+ * quest_trust_bwd_linear, with the weight's mask).
+ *
+ * Arguments
+ *   grad_y   device bf16 [T, ld_gy], the gradient of the layer output (the first N columns are
+ *            read); 16-byte aligned, ld_gy >= N a multiple of 8.
+ *   codes    device, the input's codes [T, K], 16-byte aligned: code_mode QUEST_CODES_PACKED with
+ *            bits 3..8 (4- or 8-bit containers), QUEST_CODES_INT8, or QUEST_CODES_GEMM_OPERAND and
+ *            QUEST_CODES_FP4_OPERAND (the operand bytes c of the linear layers: x_hat = bf16(c Delta / 2)).
+ *            QUEST_EUNSUPPORTED for the other forms.
+ *   scales   device fp32 [T, K / rms_group]; rms_group 128 or K.
+ *   mask     device, the weight's trust mask bits [N, K / 8] (QUEST_MASK_BITS layout), 16-byte
+ *            aligned, or NULL (every entry kept).
+ *   T, N, K  >= 0 and < 2^31; N a multiple of 8, K a multiple of 128. T == 0 is the empty sum.
+ *   had_block  128 (QUEST_EUNSUPPORTED otherwise).
+ *   grad_w   device out_dtype [N, K], 16-byte aligned; overlaps nothing.
+ *   accumulate   0: grad_w is overwritten. 1: the gradient is added to it, in fp32 (out_dtype
+ *            must be QUEST_FP32): micro-batches into one master gradient.
+ *   workspace, workspace_bytes   at least quest_weight_grad_workspace(T, N, K) bytes, 16-byte
+ *            aligned, used until the call's work on the stream is done (two calls that may run at
+ *            the same time need one each); NULL where that is 0. With few output tiles the tokens are cut
+ *            into pieces whose sums meet there, in a fixed order: results do not vary from run to run.
+ * Returns QUEST_OK, QUEST_EINVAL, QUEST_EUNSUPPORTED or QUEST_ECUDA; a bounded wait that
+ * gives up is reported by quest_device_status as QUEST_ETIMEOUT.
+ */
+quest_status quest_weight_grad(const void* grad_y, int64_t ld_gy, const void* codes, quest_code_mode code_mode,
+                               int bits, const float* scales, int64_t rms_group, const void* mask, int64_t T,
+                               int64_t N, int64_t K, int had_block, void* grad_w, quest_dtype out_dtype,
+                               int accumulate, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace quest_weight_grad needs on the current device; 0 if none (or if a size is invalid). */
+size_t quest_weight_grad_workspace(int64_t T, int64_t N, int64_t K);
+
+/*
+ * quest_lowbit_linear -- linear layer of a few tokens on 4-bit weight codes: the
+ * decoding form, where the layer is a read of the weights.
+ *
+ * Only the weights are quantized (pith.science review, Figure 4b: weight-only
+ * quantization); the input is transformed to meet them and not rounded to a grid:
+ *     xt = H x / sqrt(had_block) per block      (had_block = 0: x is in the Hadamard domain already)
+ *     y[m][n] = sum_k xt[m][k] v[n][k] Delta[n][group of k]             bf16 (RNE)
+ * with v = q + 1/2 (QUEST_CODES_PACKED, the 4-bit containers of bits 3 and 4) or the E2M1
+ * value (QUEST_CODES_FP4_PACKED). xt is held in fp16 under a power of two per token and
+ * 128 columns (relative error 2^-12 of values near the group's largest); sums are fp32. A token that
+ * holds an Inf or a NaN gives non-finite results, its own only.
+ *
+ * Arguments
+ *   x        device bf16 [M, ld_x], 16-byte aligned, ld_x >= K a multiple of 8.
+ *   w_codes  device, packed codes [N, K / 2] bytes, 16-byte aligned.
+ *   w_scales device fp32 [N, K / rms_group]; rms_group 128 or K.
+ *   M        0..64 (QUEST_EUNSUPPORTED above: quest_linear_bf16 and the code layers take over there).
+ *   N        >= 0, a multiple of 8, < 2^31.
+ *   K        0..32768, a multiple of 128 (of 256 with had_block 256). K == 0 writes zeros.
+ *   had_block  0, 16, 32, 64, 128 or 256 (the weight's).
+ *   y        device bf16 [M, N], 16-byte aligned; overlaps nothing.
+ * Returns QUEST_OK, QUEST_EINVAL, QUEST_EUNSUPPORTED or QUEST_ECUDA.
+ */
+quest_status quest_lowbit_linear(const void* x, int64_t ld_x, const void* w_codes, quest_code_mode code_mode,
+                                 const float* w_scales, int64_t rms_group, int64_t M, int64_t N, int64_t K,
+                                 int had_block, void* y, void* stream);
+
+/*
+ * quest_lowbit_gated -- the gated feed-forward block of a few tokens on 4-bit codes:
+ * quest_lowbit_linear on the gate and the up weight in one kernel,
+ *     h = act(x w_gate^T) * (x w_up^T)        (the projections in fp32, h bf16)
+ * Arguments as quest_lowbit_linear, with both weights [F, K] in one form.
+ */
+quest_status quest_lowbit_gated(const void* x, int64_t ld_x, const void* gate_codes, const float* gate_scales,
+                                const void* up_codes, const float* up_scales, quest_code_mode code_mode,
+                                int64_t rms_group, int64_t M, int64_t F, int64_t K, int had_block, quest_act act,
+                                void* h, void* stream);
+
+/*
  * quest_device_status -- synchronises `stream`, then reports (and clears) the
  * device-side status of the integer linear layer on the current device:
  * QUEST_ETIMEOUT if one of its bounded pipeline waits gave up since the last
  * call (its output is then incomplete), QUEST_OK otherwise, QUEST_ECUDA on a
  * CUDA error. The quantizer and trust kernels have no waits and never set it;
- * quest_trust_bwd_linear shares the linear layer's status word.
+ * quest_trust_bwd_linear shares the linear layer's status word. quest_gated_linear and
+ * quest_weight_grad have words of their own, reported the same way; quest_gated_bwd and the
+ * low-bit calls have no waits.
  */
 quest_status quest_device_status(void* stream);
 
