@@ -28,29 +28,61 @@ namespace {
 // is transposed or dequantised in HBM.
 //
 // CTA pairs, M = 256 rows of G, N = 256 columns, K = 16 tokens per MMA, 64 tokens per stage.
-// Roles per CTA: one warp loads gy tiles by TMA, one loads the raw codes by TMA into a ring of their own, four
-// warps turn codes into the bf16 B tile (byte -> fp32 by a byte permute onto 2^15, minus the
-// offset, times the token's step, rounded to bf16 as the quantizer's dequant is), one
-// thread of the even CTA issues the MMAs, four warps run the epilogue.
-constexpr int kWThreads = 352;
-constexpr int kConvWarps = 4;
+// Five warpgroups per CTA: one whose warps load gy tiles by TMA, load the raw codes by TMA into a
+// ring of their own, and (in the even CTA) issue the MMAs; two that turn codes into the bf16 B tile,
+// alternating stages (byte -> fp32 by a byte permute onto 2^15, minus the offset, times the
+// token's step, rounded to bf16 as the quantizer's dequant is); two epilogue teams, one per 128-column
+// half. Registers move from the first three to the teams (setmaxnreg).
+//
+// The tensor core adds to its fp32 accumulator by cutting, so a sum of T / 16 steps drifts by about
+// T / 16 * 2^-25. Each accumulator therefore holds only kSegBlocks blocks (512 tokens, 32 steps);
+// the teams add it to fp32 registers, rounding to nearest, while the MMAs fill the other one.
+constexpr int kWThreads = 640;
+constexpr int kConvWarps = 4;                              // per conversion group
+constexpr int kTeamThreads = 128;
+constexpr int kSegBlocks = 8;
 constexpr int kTokens = 64;                                // tokens per stage
 constexpr uint32_t kWBox = kTokens * 128;                  // one 64-column box: 64 rows of 128 bytes
 constexpr int kWStages = 5;
-constexpr int kRawStages = 5;
+constexpr int kRawStages = 4;
 constexpr uint32_t kWStageA = 2 * kWBox, kWStageB = 2 * kWBox;
 constexpr uint32_t kRawBytes = kTokens * 128;              // 8-bit codes of 128 columns (half of it for 4 bits)
-constexpr uint32_t kWChunk = BM * 64;                      // epilogue staging: 128 rows of 64 bytes
+constexpr uint32_t kWChunk = BM * 64;                      // epilogue staging: 128 rows of 64 bytes, two a team
 constexpr uint32_t kWSmemA = 0;
 constexpr uint32_t kWSmemB = kWSmemA + kWStages * kWStageA;
 constexpr uint32_t kWSmemRaw = kWSmemB + kWStages * kWStageB;
 constexpr uint32_t kWSmemC = kWSmemRaw + kRawStages * kRawBytes;
-constexpr uint32_t kWSmemBar = kWSmemC + 2 * kWChunk;
+constexpr uint32_t kWSmemBar = kWSmemC + 4 * kWChunk;
 constexpr uint32_t kWNumBars = 3 * kWStages + 2 * kRawStages + 4 + 1;
 constexpr uint32_t kWSmemTmemSlot = kWSmemBar + kWNumBars * 8;
 constexpr uint32_t kWSmemAbort = kWSmemTmemSlot + 4;
 constexpr uint32_t kWSmemTotal = kWSmemAbort + 4 + 1024;
 static_assert(kWSmemTotal <= 227 * 1024, "weight gradient shared memory");
+
+// Registers per thread of the three kinds of warpgroup: 128 * (24 + 2 * 48 + 2 * 176) = 60416 of the 61440
+// (640 * 96) the block is launched with.
+constexpr int kRegsIssue = 24, kRegsConv = 48, kRegsTeam = 176;
+static_assert(128 * (kRegsIssue + 2 * kRegsConv + 2 * kRegsTeam) <= kWThreads * 96, "register split");
+template <int N>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
+__device__ __forceinline__ void team_bar(int id) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kTeamThreads) : "memory");
+}
+__device__ __forceinline__ bool team_any(int id, bool pred) {
+    uint32_t out;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, %2, %3, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(out)
+        : "r"((uint32_t)pred), "r"(id), "n"(kTeamThreads)
+        : "memory");
+    return out != 0;
+}
 
 constexpr uint32_t kIdescBf16Mn = (1u << 4)      // D: fp32
                                 | (1u << 7)      // A: bf16
@@ -79,39 +111,6 @@ __device__ __forceinline__ void tc_mma_bf16_mn_pair(uint32_t d_tmem, uint64_t ad
         "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(adesc), "l"(bdesc), "r"(kIdescBf16Mn), "r"(accumulate)
         : "memory");
-}
-
-// Arrival on the even CTA's barrier that publishes this warp's tile stores (already fenced
-// for the async proxy) to the MMA issuer, and the issuer's matching wait: cluster scope, since
-// the writers may be in the odd CTA.
-__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(kSuspendMmaNs)
-        : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
-    for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait_cluster(bar, parity)) return true;
-        if ((it & 63u) == 0) {
-            if (*abort_flag) return false;
-            if (global_timer_ns() - t0 > kWaitLimitNs) {
-                *abort_flag = 1;
-                atomicExch(&g_tc_status, (int)QUEST_ETIMEOUT);
-                return false;
-            }
-        }
-    }
 }
 
 __device__ __forceinline__ void tma_reduce_add_2d(const CUtensorMap* map, uint32_t src, int c0, int c1) {
@@ -208,7 +207,7 @@ weight_grad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_const
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar_tfull + 8 * b, 1);
-            mbar_init(bar_tempty + 8 * b, 2);
+            mbar_init(bar_tempty + 8 * b, 4);   // two teams in each CTA
         }
         mbar_init(bar_drain, 1);
         *abort_flag = 0;
@@ -227,7 +226,9 @@ weight_grad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_const
     pdl_wait();
     pdl_trigger();
 
-    if (warp == 0) {
+    if (warp < 4) {
+      regs_dec<kRegsIssue>();
+      if (warp == 0) {
         // ------------------------------------------------------------ gy producer (both CTAs)
         if (lane == 0) {
             const uint32_t full_even = map_to_rank(bar_fulla, 0);
@@ -271,36 +272,38 @@ weight_grad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_const
         if (even && lane == 0) {
             uint32_t stage = 0, phase = 0;
             bool ok = true;
-            int local = 0;
-            for (int item = pair; item < num_items && ok; item += num_pairs, ++local) {
+            int local = 0;   // segments so far
+            for (int item = pair; item < num_items && ok; item += num_pairs) {
                 const int split = item / tiles;
                 const int tb0 = split * p.blocks_per_split, tb1 = min(tb0 + p.blocks_per_split, p.num_tb);
-                const uint32_t buf = local & 1, bphase = (local >> 1) & 1;
-                if (!mbar_wait(bar_tempty + 8 * buf, bphase ^ 1, abort_flag, kWaitLimitNs, kSuspendMmaNs)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t d_tmem = tmem_base + buf * BN;
-                for (int tb = tb0; tb < tb1; ++tb) {
-                    if (!mbar_wait(bar_fulla + 8 * stage, phase, abort_flag, kWaitLimitNs, kSuspendMmaNs) ||
-                        !mbar_wait_cluster(bar_fullb + 8 * stage, phase, abort_flag)) {
+                for (int seg = tb0; seg < tb1 && ok; seg += kSegBlocks, ++local) {
+                    const int seg_end = min(seg + kSegBlocks, tb1);
+                    const uint32_t buf = local & 1, bphase = (local >> 1) & 1;
+                    if (!mbar_wait(bar_tempty + 8 * buf, bphase ^ 1, abort_flag, kWaitLimitNs, kSuspendMmaNs)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t a_addr = sbase + kWSmemA + stage * kWStageA;
-                    const uint32_t b_addr = sbase + kWSmemB + stage * kWStageB;
+                    const uint32_t d_tmem = tmem_base + buf * BN;
+                    for (int tb = seg; tb < seg_end; ++tb) {
+                        if (!mbar_wait(bar_fulla + 8 * stage, phase, abort_flag, kWaitLimitNs, kSuspendMmaNs) ||
+                            !mbar_wait(bar_fullb + 8 * stage, phase, abort_flag, kWaitLimitNs, kSuspendMmaNs)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t a_addr = sbase + kWSmemA + stage * kWStageA;
+                        const uint32_t b_addr = sbase + kWSmemB + stage * kWStageB;
 #pragma unroll
-                    for (int kk = 0; kk < kTokens / 16; ++kk) {
-                        tc_mma_bf16_mn_pair(d_tmem, smem_desc_mn128(a_addr + kk * 2048),
-                                            smem_desc_mn128(b_addr + kk * 2048), tb != tb0 || kk != 0);
+                        for (int kk = 0; kk < kTokens / 16; ++kk) {
+                            tc_mma_bf16_mn_pair(d_tmem, smem_desc_mn128(a_addr + kk * 2048),
+                                                smem_desc_mn128(b_addr + kk * 2048), tb != seg || kk != 0);
+                        }
+                        tc_commit_pair_mc(bar_empty + 8 * stage);
+                        if (++stage == kWStages) { stage = 0; phase ^= 1; }
                     }
-                    tc_commit_pair_mc(bar_empty + 8 * stage);
-                    if (++stage == kWStages) { stage = 0; phase ^= 1; }
+                    if (ok) tc_commit_pair_mc(bar_tfull + 8 * buf);
                 }
-                if (!ok) break;
-                tc_commit_pair_mc(bar_tfull + 8 * buf);
             }
             tc_commit_pair(bar_drain);
             const uint64_t t0 = global_timer_ns();
@@ -339,56 +342,54 @@ weight_grad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_const
                 }
             }
         }
-    } else if (warp < 3 + kConvWarps) {
-        // ------------------------------------------------------------ code conversion (warps 3..6, both CTAs)
-        const int cw = warp - 3;
+      }
+    } else if (warp < 12) {
+        // ------------------------------------------------------------ code conversion (warps 4..11, both CTAs)
+        regs_dec<kRegsConv>();
+        const int group = (warp - 4) >> 2, cw = warp & 3;   // the group converts every second block of the pair
         const int t = (cw & 1) * 32 + lane;    // token of the block
         const int half = cw >> 1;              // 64-column box of the CTA's 128 columns
         const uint32_t fullb_even = map_to_rank(bar_fullb, 0);
         const float2 neg_off = make_float2(-p.offset, -p.offset);
-        uint32_t stage = 0, phase = 0, rstage = 0, rphase = 0;
+        uint32_t stage = group, phase = 0, rstage = group, rphase = 0;
+        int done = 0;                          // blocks of the items so far
         bool ok = true;
         for (int item = pair; item < num_items && ok; item += num_pairs) {
             const int tile = item % tiles, split = item / tiles;
             const int k0 = (tile % p.num_k) * BN + 128 * int(rank);
             const int tb0 = split * p.blocks_per_split, tb1 = min(tb0 + p.blocks_per_split, p.num_tb);
-            // this token's step, fetched one block ahead; 0 past the last token or column, where
+            // this token's step, fetched one turn ahead; 0 past the last token or column, where
             // the codes read as zero too
             const float* sc = p.scales + (p.scale_stride == 1 ? 0 : k0 / 128);
             auto step_of = [&](int tb) {
                 const int64_t tok = int64_t(tb) * kTokens + t;
                 return tok < p.T && k0 < p.K && tb < tb1 ? __ldg(sc + tok * p.scale_stride) * p.mul : 0.0f;
             };
-            float next = step_of(tb0);
-            for (int tb = tb0; tb < tb1; ++tb) {
+            int tb = tb0 + ((group ^ done) & 1);
+            done += tb1 - tb0;
+            float next = step_of(tb);
+            for (; tb < tb1; tb += 2) {
                 const float2 step = make_float2(next, next);
-                next = step_of(tb + 1);
+                next = step_of(tb + 2);
                 // (giving up is decided by the whole warp: its lanes meet again below)
                 if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar_rfull + 8 * rstage, rphase, abort_flag, kWaitLimitNs,
+                                                       kSuspendProducerNs)) ||
+                    !__all_sync(0xFFFFFFFFu, mbar_wait(bar_empty + 8 * stage, phase ^ 1, abort_flag, kWaitLimitNs,
                                                        kSuspendProducerNs))) {
                     ok = false;
                     break;
                 }
                 const uint32_t raw = sbase + kWSmemRaw + rstage * kRawBytes;
-                uint4 q[4];
+                const uint32_t row = sbase + kWSmemB + stage * kWStageB + half * kWBox + t * 128;
 #pragma unroll
                 for (int j = 0; j < CB / 2; ++j) {
                     const uint32_t at = CB == 8 ? raw + t * 128 + (((half * 4 + j) ^ (t & 7)) << 4)
                                                 : raw + t * 64 + (((half * 2 + j) ^ ((t >> 1) & 3)) << 4);
+                    uint32_t w[4];
                     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                                 : "=r"(q[j].x), "=r"(q[j].y), "=r"(q[j].z), "=r"(q[j].w)
+                                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                                  : "r"(at)
                                  : "memory");
-                }
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar_empty + 8 * stage, phase ^ 1, abort_flag, kWaitLimitNs,
-                                                       kSuspendProducerNs))) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t row = sbase + kWSmemB + stage * kWStageB + half * kWBox + t * 128;
-#pragma unroll
-                for (int j = 0; j < CB / 2; ++j) {
-                    const uint32_t w[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
                     if constexpr (CB == 8) {
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
@@ -421,112 +422,122 @@ weight_grad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_const
                     // the raw slot is returned only now that its values have arrived and been used: an arrival
                     // right behind the loads does not wait for them, and rarely let the next copy overtake one
                     mbar_arrive(bar_rempty + 8 * rstage);
-                    mbar_arrive_release_cluster(fullb_even + 8 * stage);
+                    mbar_arrive_remote(fullb_even + 8 * stage);
                 }
-                if (++rstage == kRawStages) { rstage = 0; rphase ^= 1; }
-                if (++stage == kWStages) { stage = 0; phase ^= 1; }
+                rstage += 2;
+                if (rstage >= kRawStages) { rstage -= kRawStages; rphase ^= 1; }
+                stage += 2;
+                if (stage >= kWStages) { stage -= kWStages; phase ^= 1; }
             }
         }
     } else {
-        // ------------------------------------------------------------ epilogue (warps 7..10, both CTAs)
-        const int et = threadIdx.x - 32 * (3 + kConvWarps);
+        // ------------------------------------------------------------ epilogue teams (warps 12..19, both CTAs)
+        regs_inc<kRegsTeam>();
+        const int team = (warp - 12) >> 2;     // 128-column half of the tile
+        const int et = threadIdx.x - 32 * (12 + 4 * team), bar_id = 1 + team;
         const int quarter = warp & 3;
         const int row_in_tile = quarter * 32 + lane;
         const uint32_t lane_addr = uint32_t(quarter * 32) << 16;
         const uint32_t tempty_even = map_to_rank(bar_tempty, 0);
+        const uint32_t staging = sbase + kWSmemC + team * 2 * kWChunk;
         int local = 0;
         int cbuf = 0;
-        for (int item = pair; item < num_items; item += num_pairs, ++local) {
+        bool ok = true;
+        for (int item = pair; item < num_items && ok; item += num_pairs) {
             const int tile = item % tiles, split = item / tiles;
-            const int n0 = (tile / p.num_k) * 256 + 128 * int(rank), k0 = (tile % p.num_k) * BN;
-            const uint32_t buf = local & 1, bphase = (local >> 1) & 1;
-            const int n = n0 + row_in_tile;
-            uint4 mw[2] = {make_uint4(~0u, ~0u, ~0u, ~0u), make_uint4(~0u, ~0u, ~0u, ~0u)};
-            if (OUT != kOutRaw && p.mask != nullptr) {
+            const int n0 = (tile / p.num_k) * 256 + 128 * int(rank), k0 = (tile % p.num_k) * BN + 128 * team;
+            const int tb0 = split * p.blocks_per_split, tb1 = min(tb0 + p.blocks_per_split, p.num_tb);
+            float2 w[64];
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const int kb0 = k0 + 128 * b;
-                    if (n < p.N && kb0 < p.K)
-                        mw[b] = *reinterpret_cast<const uint4*>(p.mask + int64_t(n) * (p.K / 8) + kb0 / 8);
-                }
-            }
-            const bool got = mbar_wait(bar_tfull + 8 * buf, bphase, abort_flag, kWaitLimitNs, kSuspendEpilogueNs);
-            if (epi_any(!got)) break;
-            tc_fence_after();
-            const uint32_t t_acc = tmem_base + lane_addr + buf * BN;
+            for (int i = 0; i < 64; ++i) w[i] = make_float2(0.0f, 0.0f);
 #pragma unroll 1
-            for (int b = 0; b < 2; ++b) {
-                if (n0 >= p.N || k0 + 128 * b >= p.K) break;   // nothing of this block is stored (uniform)
-                const uint4 mb = b == 0 ? mw[0] : mw[1];
-                float2 w[64];
+            for (int seg = tb0; seg < tb1; seg += kSegBlocks, ++local) {
+                const uint32_t buf = local & 1, bphase = (local >> 1) & 1;
+                const bool got = mbar_wait(bar_tfull + 8 * buf, bphase, abort_flag, kWaitLimitNs, kSuspendEpilogueNs);
+                if (team_any(bar_id, !got)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t t_acc = tmem_base + lane_addr + buf * BN + 128 * team;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t r[32];
-                    QUEST_TMEM_LD32(t_acc + 128 * b + 32 * c, r);
+                for (int c = 0; c < 8; ++c) {
+                    uint32_t r[16];
+                    QUEST_TMEM_LD16(t_acc + 16 * c, r);
                     tmem_wait_ld();
-                    const uint32_t bits = c == 0 ? mb.x : c == 1 ? mb.y : c == 2 ? mb.z : mb.w;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        if constexpr (OUT != kOutRaw) {
-                            const uint32_t k0m = 0u - ((bits >> (2 * i)) & 1u);
-                            const uint32_t k1m = 0u - ((bits >> (2 * i + 1)) & 1u);
-                            w[16 * c + i] =
-                                make_float2(__uint_as_float(r[2 * i] & k0m), __uint_as_float(r[2 * i + 1] & k1m));
-                        } else {
-                            w[16 * c + i] = make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-                        }
-                    }
+                    for (int i = 0; i < 8; ++i)
+                        w[8 * c + i] = __fadd2_rn(w[8 * c + i], make_float2(__uint_as_float(r[2 * i]),
+                                                                            __uint_as_float(r[2 * i + 1])));
                 }
-                if constexpr (OUT != kOutRaw) fwht128(w);
-                constexpr int kChunks = OUT == kOutBf16 ? 4 : 8;   // of 64 bytes a row: 32 bf16 or 16 fp32 columns
-                constexpr float kScale = OUT == kOutRaw ? 1.0f : kInvSqrt128;
-#pragma unroll
-                for (int c = 0; c < kChunks; ++c) {
-                    const uint32_t stg = sbase + kWSmemC + cbuf * kWChunk + row_in_tile * 64;
-                    const uint32_t swz = (row_in_tile >> 1) & 3;
-#pragma unroll
-                    for (int q16 = 0; q16 < 4; ++q16) {
-                        uint32_t o[4];
-                        if constexpr (OUT == kOutBf16) {
-#pragma unroll
-                            for (int h = 0; h < 4; ++h) {
-                                const float2 v = w[16 * c + 4 * q16 + h];
-                                const __nv_bfloat162 hb = __floats2bfloat162_rn(v.x * kScale, v.y * kScale);
-                                o[h] = *reinterpret_cast<const uint32_t*>(&hb);
-                            }
-                        } else {
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const float2 v = w[8 * c + 2 * q16 + h];
-                                o[2 * h] = __float_as_uint(v.x * kScale);
-                                o[2 * h + 1] = __float_as_uint(v.y * kScale);
-                            }
-                        }
-                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(stg + ((q16 ^ swz) << 4)),
-                                     "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
-                                     : "memory");
-                    }
-                    fence_proxy_async_smem();
-                    epi_bar();
-                    if (et == 0) {
-                        const int col = k0 + 128 * b + c * (128 / kChunks);
-                        const uint32_t src = sbase + kWSmemC + cbuf * kWChunk;
-                        if (OUT == kOutRaw)
-                            tma_store_2d(&map_o, src, col, split * p.raw_rows + n0);
-                        else if (OUT == kOutF32 && p.add)
-                            tma_reduce_add_2d(&map_o, src, col, n0);
-                        else
-                            tma_store_2d(&map_o, src, col, n0);
-                        bulk_commit();
-                        bulk_wait_read_le1();
-                    }
-                    epi_bar();
-                    cbuf ^= 1;
-                }
+                tc_fence_before();
+                team_bar(bar_id);
+                if (et == 0) mbar_arrive_remote(tempty_even + 8 * buf);
             }
-            tc_fence_before();
-            epi_bar();
-            if (et == 0) mbar_arrive_remote(tempty_even + 8 * buf);
+            if (!ok) break;
+            if (n0 >= p.N || k0 >= p.K) continue;   // nothing of this half is stored (the same for the whole team)
+            if constexpr (OUT != kOutRaw) {
+                const int n = n0 + row_in_tile;
+                if (p.mask != nullptr && n < p.N) {
+                    const uint4 mb = *reinterpret_cast<const uint4*>(p.mask + int64_t(n) * (p.K / 8) + k0 / 8);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t bits = c == 0 ? mb.x : c == 1 ? mb.y : c == 2 ? mb.z : mb.w;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float2& v = w[16 * c + i];
+                            v.x = (bits >> (2 * i)) & 1u ? v.x : 0.0f;
+                            v.y = (bits >> (2 * i + 1)) & 1u ? v.y : 0.0f;
+                        }
+                    }
+                }
+                fwht128(w);
+            }
+            constexpr int kChunks = OUT == kOutBf16 ? 4 : 8;   // of 64 bytes a row: 32 bf16 or 16 fp32 columns
+            constexpr float kScale = OUT == kOutRaw ? 1.0f : kInvSqrt128;
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                const uint32_t stg = staging + cbuf * kWChunk + row_in_tile * 64;
+                const uint32_t swz = (row_in_tile >> 1) & 3;
+#pragma unroll
+                for (int q16 = 0; q16 < 4; ++q16) {
+                    uint32_t o[4];
+                    if constexpr (OUT == kOutBf16) {
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            const float2 v = w[16 * c + 4 * q16 + h];
+                            const __nv_bfloat162 hb = __floats2bfloat162_rn(v.x * kScale, v.y * kScale);
+                            o[h] = *reinterpret_cast<const uint32_t*>(&hb);
+                        }
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float2 v = w[8 * c + 2 * q16 + h];
+                            o[2 * h] = __float_as_uint(v.x * kScale);
+                            o[2 * h + 1] = __float_as_uint(v.y * kScale);
+                        }
+                    }
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(stg + ((q16 ^ swz) << 4)), "r"(o[0]),
+                                 "r"(o[1]), "r"(o[2]), "r"(o[3])
+                                 : "memory");
+                }
+                fence_proxy_async_smem();
+                team_bar(bar_id);
+                if (et == 0) {
+                    const int col = k0 + c * (128 / kChunks);
+                    const uint32_t src = staging + cbuf * kWChunk;
+                    if (OUT == kOutRaw)
+                        tma_store_2d(&map_o, src, col, split * p.raw_rows + n0);
+                    else if (OUT == kOutF32 && p.add)
+                        tma_reduce_add_2d(&map_o, src, col, n0);
+                    else
+                        tma_store_2d(&map_o, src, col, n0);
+                    bulk_commit();
+                    bulk_wait_read_le1();
+                }
+                team_bar(bar_id);
+                cbuf ^= 1;
+            }
         }
         if (et == 0) bulk_wait_all();
     }
