@@ -207,7 +207,7 @@ def weight_grad_raw(grad_y, ld_gy, codes, code_mode, bits, scales, rms_group, ma
 
 
 def weight_grad_workspace(T: int, N: int, K: int) -> int:
-    """Bytes of workspace weight_grad_raw needs on the current device (0: none)."""
+    """Bytes of workspace weight_grad_raw needs on the current device."""
     return int(load_library().quest_weight_grad_workspace(T, N, K))
 
 

@@ -22,47 +22,47 @@ namespace {
 //   G[n][k]  = sum_t gy[t][n] xh[t][k],  xh[t][k] = bf16((q[t][k] + 1/2) Delta[t][group of k])
 //   gw[n][b] = H (mask[n][b] * G[n][b]) / sqrt(128)   per 128-column block b of a row
 //
+// Two launches. A streaming pass restores xh into the workspace (byte -> fp32 by a byte permute
+// onto 2^15, minus the offset, times the token's step, rounded to bf16 as the quantizer's dequant
+// is): 3 bytes moved per value. The product then runs at the tensor cores' rate. Restoring inside
+// the product's mainloop instead repeats the work for every 256 rows of G: eight conversion warps
+// beside the MMAs took 694 us at 16384 x 11264 x 2048, of which 190 us went away with the
+// conversion's arithmetic and stores taken out; the pass costs about 20.
+//
 // The reduction runs over the tokens, the outer dimension of both operands, so the MMA
 // takes both transposed (MN-major): a stage row is one token's 64 columns (128 bytes,
-// 128-byte swizzle), which is how gy [T, N] and the codes [T, K] lie in memory. Nothing
-// is transposed or dequantised in HBM.
+// 128-byte swizzle), which is how gy [T, N] and xh [T, K] lie in memory. Nothing is transposed.
 //
 // CTA pairs, M = 256 rows of G, N = 256 columns, K = 16 tokens per MMA, 64 tokens per stage.
-// Five warpgroups per CTA: one whose warps load gy tiles by TMA, load the raw codes by TMA into a
-// ring of their own, and (in the even CTA) issue the MMAs; two that turn codes into the bf16 B tile,
-// alternating stages (byte -> fp32 by a byte permute onto 2^15, minus the offset, times the
-// token's step, rounded to bf16 as the quantizer's dequant is); two epilogue teams, one per 128-column
-// half. Registers move from the first three to the teams (setmaxnreg).
+// Three warpgroups per CTA: one holds the TMA producer and (in the even CTA) the MMA issuer,
+// two are epilogue teams, one per 128-column half; registers move to the teams (setmaxnreg).
 //
 // The tensor core adds to its fp32 accumulator by cutting, so a sum of T / 16 steps drifts by about
-// T / 16 * 2^-25. Each accumulator therefore holds only kSegBlocks blocks (512 tokens, 32 steps);
+// T / 16 * 2^-26 of its value. An accumulator therefore holds at most one segment of the tokens;
 // the teams add it to fp32 registers, rounding to nearest, while the MMAs fill the other one.
-constexpr int kWThreads = 640;
-constexpr int kConvWarps = 4;                              // per conversion group
+// Segments of 512 tokens keep an fp32 gradient within 6e-7 (2-norm; 4.3e-6 for 4096 tokens
+// without them); a bf16 gradient is off by 1.7e-3 through its own rounding, and takes segments of 4096.
+constexpr int kWThreads = 384;
 constexpr int kTeamThreads = 128;
-constexpr int kSegBlocks = 8;
 constexpr int kTokens = 64;                                // tokens per stage
+constexpr int kSegF32 = 512 / kTokens, kSegBf16 = 4096 / kTokens;
 constexpr uint32_t kWBox = kTokens * 128;                  // one 64-column box: 64 rows of 128 bytes
-constexpr int kWStages = 5;
-constexpr int kRawStages = 4;
+constexpr int kWStages = 6;
 constexpr uint32_t kWStageA = 2 * kWBox, kWStageB = 2 * kWBox;
-constexpr uint32_t kRawBytes = kTokens * 128;              // 8-bit codes of 128 columns (half of it for 4 bits)
 constexpr uint32_t kWChunk = BM * 64;                      // epilogue staging: 128 rows of 64 bytes, two a team
 constexpr uint32_t kWSmemA = 0;
 constexpr uint32_t kWSmemB = kWSmemA + kWStages * kWStageA;
-constexpr uint32_t kWSmemRaw = kWSmemB + kWStages * kWStageB;
-constexpr uint32_t kWSmemC = kWSmemRaw + kRawStages * kRawBytes;
+constexpr uint32_t kWSmemC = kWSmemB + kWStages * kWStageB;
 constexpr uint32_t kWSmemBar = kWSmemC + 4 * kWChunk;
-constexpr uint32_t kWNumBars = 3 * kWStages + 2 * kRawStages + 4 + 1;
+constexpr uint32_t kWNumBars = 2 * kWStages + 4 + 1;
 constexpr uint32_t kWSmemTmemSlot = kWSmemBar + kWNumBars * 8;
 constexpr uint32_t kWSmemAbort = kWSmemTmemSlot + 4;
 constexpr uint32_t kWSmemTotal = kWSmemAbort + 4 + 1024;
 static_assert(kWSmemTotal <= 227 * 1024, "weight gradient shared memory");
 
-// Registers per thread of the three kinds of warpgroup: 128 * (24 + 2 * 48 + 2 * 176) = 60416 of the 61440
-// (640 * 96) the block is launched with.
-constexpr int kRegsIssue = 24, kRegsConv = 48, kRegsTeam = 176;
-static_assert(128 * (kRegsIssue + 2 * kRegsConv + 2 * kRegsTeam) <= kWThreads * 96, "register split");
+// Registers per thread: 128 * (56 + 2 * 224) = 64512, what the block is launched with (384 * 168).
+constexpr int kRegsIssue = 56, kRegsTeam = 224;
+static_assert(128 * (kRegsIssue + 2 * kRegsTeam) <= kWThreads * 168, "register split");
 template <int N>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -122,11 +122,6 @@ __device__ __forceinline__ void tma_reduce_add_2d(const CUtensorMap* map, uint32
 
 struct WeightGradParams {
     const uint8_t* mask;        // trust mask bits of the weight [N, K / 8], or null (all kept)
-    const float* scales;        // [T, groups]
-    int64_t scale_stride;       // groups: 1 (a step per token) or K / 128
-    float offset;               // code byte as unsigned -> value: (2^15 + u) - offset, times step * mul
-    float mul;
-    uint32_t flip;              // makes the stored two's complement fields unsigned
     int T, N, K;
     int num_n, num_k;           // 256-row and 256-column tiles of G
     int splits, blocks_per_split, num_tb;   // token blocks of 64: in all, and per split
@@ -168,22 +163,79 @@ __device__ __forceinline__ void convert4(uint32_t u, float2 neg_off, float2 step
     hi = *reinterpret_cast<const uint32_t*>(&hb);
 }
 
-// CB: bits of a stored code (8 or 4). OUT: kOutBf16 / kOutF32 finish the gradient; kOutRaw
-// stores the plain sums of one token split for weight_grad_finish_kernel.
-template <int CB, int OUT>
+// The saved codes restored to bf16: xh [T, K], 16 code bytes a thread (16 or 32 values).
+struct RestoreParams {
+    const uint4* codes;
+    const float* scales;
+    uint4* xh;
+    int64_t chunks;             // T * per_row
+    int per_row;                // 16-byte chunks per token
+    int scale_shift;            // chunk index in the row >> shift = group (31: one step per token)
+    int64_t groups;
+    float offset;               // code byte as unsigned -> value: (2^15 + u) - offset, times step * mul
+    float mul;
+    uint32_t flip;              // makes the stored two's complement fields unsigned
+};
+
+template <int CB>
+__global__ void __launch_bounds__(256) restore_codes_kernel(const RestoreParams p) {
+    pdl_wait();
+    pdl_trigger();
+    const float2 neg_off = make_float2(-p.offset, -p.offset);
+    const int64_t stride = int64_t(gridDim.x) * blockDim.x;
+    int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
+    int64_t row = i / p.per_row;
+    int at = int(i - row * p.per_row);
+    const int64_t row_step = stride / p.per_row;
+    const int at_step = int(stride - row_step * p.per_row);
+    for (; i < p.chunks; i += stride) {
+        const uint4 q = __ldcs(p.codes + i);
+        const float s = __ldg(p.scales + row * p.groups + (at >> p.scale_shift)) * p.mul;
+        const float2 step = make_float2(s, s);
+        const uint32_t w[4] = {q.x ^ p.flip, q.y ^ p.flip, q.z ^ p.flip, q.w ^ p.flip};
+        uint4* out = p.xh + i * (16 / CB);
+        if constexpr (CB == 8) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t o[4];
+                convert4(w[2 * h], neg_off, step, o[0], o[1]);
+                convert4(w[2 * h + 1], neg_off, step, o[2], o[3]);
+                out[h] = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+        } else {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                // low nibbles are the even elements, high nibbles the odd ones
+                const uint32_t ev = w[h] & 0x0F0F0F0Fu, od = (w[h] >> 4) & 0x0F0F0F0Fu;
+                uint32_t o[4];
+                convert4(__byte_perm(ev, od, 0x5140), neg_off, step, o[0], o[1]);
+                convert4(__byte_perm(ev, od, 0x7362), neg_off, step, o[2], o[3]);
+                out[h] = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+        }
+        row += row_step;
+        at += at_step;
+        if (at >= p.per_row) {
+            at -= p.per_row;
+            ++row;
+        }
+    }
+}
+
+// OUT: kOutBf16 / kOutF32 finish the gradient; kOutRaw stores the plain sums of one token
+// split for weight_grad_finish_kernel.
+template <int OUT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWThreads, 1)
-weight_grad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_constant__ CUtensorMap map_q,
+weight_grad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_constant__ CUtensorMap map_x,
                    const __grid_constant__ CUtensorMap map_o, const WeightGradParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
-    const uint32_t bar_fulla = sbase + kWSmemBar;                // [kWStages] gy landed (even CTA)
-    const uint32_t bar_fullb = bar_fulla + 8 * kWStages;         // [kWStages] B tile converted (even CTA)
-    const uint32_t bar_empty = bar_fullb + 8 * kWStages;         // [kWStages] MMAs done with the stage
-    const uint32_t bar_rfull = bar_empty + 8 * kWStages;         // [kRawStages] raw codes landed
-    const uint32_t bar_rempty = bar_rfull + 8 * kRawStages;      // [kRawStages] raw codes read
-    const uint32_t bar_tfull = bar_rempty + 8 * kRawStages;      // [2]
-    const uint32_t bar_tempty = bar_tfull + 16;                  // [2] (even CTA)
+    constexpr int kSeg = OUT == kOutBf16 ? kSegBf16 : kSegF32;
+    const uint32_t bar_full = sbase + kWSmemBar;                 // [kWStages], used in the even CTA
+    const uint32_t bar_empty = bar_full + 8 * kWStages;          // [kWStages]
+    const uint32_t bar_tfull = bar_empty + 8 * kWStages;         // [2]
+    const uint32_t bar_tempty = bar_tfull + 16;                  // [2], used in the even CTA
     const uint32_t bar_drain = bar_tempty + 16;                  // [1]
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kWSmemAbort);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kWSmemTmemSlot);
@@ -197,13 +249,8 @@ weight_grad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_const
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kWStages; ++s) {
-            mbar_init(bar_fulla + 8 * s, 1);
-            mbar_init(bar_fullb + 8 * s, 2 * kConvWarps);
+            mbar_init(bar_full + 8 * s, 1);
             mbar_init(bar_empty + 8 * s, 1);
-        }
-        for (int s = 0; s < kRawStages; ++s) {
-            mbar_init(bar_rfull + 8 * s, 1);
-            mbar_init(bar_rempty + 8 * s, kConvWarps);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar_tfull + 8 * b, 1);
@@ -229,25 +276,29 @@ weight_grad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_const
     if (warp < 4) {
       regs_dec<kRegsIssue>();
       if (warp == 0) {
-        // ------------------------------------------------------------ gy producer (both CTAs)
+        // ------------------------------------------------------------ TMA producer (both CTAs)
         if (lane == 0) {
-            const uint32_t full_even = map_to_rank(bar_fulla, 0);
+            const uint32_t full_even = map_to_rank(bar_full, 0);
             uint32_t stage = 0, phase = 0;
             uint64_t issued = 0;
             bool ok = true;
             for (int item = pair; item < num_items && ok; item += num_pairs) {
                 const int tile = item % tiles, split = item / tiles;
                 const int n0 = (tile / p.num_k) * 256 + 128 * int(rank);
+                const int k0 = (tile % p.num_k) * BN + 128 * int(rank);
                 const int tb0 = split * p.blocks_per_split, tb1 = min(tb0 + p.blocks_per_split, p.num_tb);
                 for (int tb = tb0; tb < tb1; ++tb) {
                     if (!mbar_wait(bar_empty + 8 * stage, phase ^ 1, abort_flag, kWaitLimitNs, kSuspendProducerNs)) {
                         ok = false;
                         break;
                     }
-                    if (even) mbar_arrive_expect_tx(bar_fulla + 8 * stage, 2 * kWStageA);
-                    const uint32_t fb = full_even + 8 * stage, dst = sbase + kWSmemA + stage * kWStageA;
-                    tma_load_2d_pair(dst, &map_g, n0, tb * kTokens, fb);
-                    tma_load_2d_pair(dst + kWBox, &map_g, n0 + 64, tb * kTokens, fb);
+                    if (even) mbar_arrive_expect_tx(bar_full + 8 * stage, 2 * (kWStageA + kWStageB));
+                    const uint32_t fb = full_even + 8 * stage;
+                    const uint32_t a_dst = sbase + kWSmemA + stage * kWStageA, b_dst = sbase + kWSmemB + stage * kWStageB;
+                    tma_load_2d_pair(a_dst, &map_g, n0, tb * kTokens, fb);
+                    tma_load_2d_pair(a_dst + kWBox, &map_g, n0 + 64, tb * kTokens, fb);
+                    tma_load_2d_pair(b_dst, &map_x, k0, tb * kTokens, fb);
+                    tma_load_2d_pair(b_dst + kWBox, &map_x, k0 + 64, tb * kTokens, fb);
                     ++issued;
                     if (++stage == kWStages) { stage = 0; phase ^= 1; }
                 }
@@ -258,7 +309,7 @@ weight_grad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_const
                 for (uint64_t i = issued - n; i < issued; ++i) {
                     const uint32_t st = uint32_t(i % kWStages), ph = uint32_t((i / kWStages) & 1);
                     const uint64_t t0 = global_timer_ns();
-                    while (!mbar_try_wait(bar_fulla + 8 * st, ph) && global_timer_ns() - t0 < kWaitLimitNs) {
+                    while (!mbar_try_wait(bar_full + 8 * st, ph) && global_timer_ns() - t0 < kWaitLimitNs) {
                     }
                 }
             } else if (!ok) {
@@ -276,8 +327,8 @@ weight_grad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_const
             for (int item = pair; item < num_items && ok; item += num_pairs) {
                 const int split = item / tiles;
                 const int tb0 = split * p.blocks_per_split, tb1 = min(tb0 + p.blocks_per_split, p.num_tb);
-                for (int seg = tb0; seg < tb1 && ok; seg += kSegBlocks, ++local) {
-                    const int seg_end = min(seg + kSegBlocks, tb1);
+                for (int seg = tb0; seg < tb1 && ok; seg += kSeg, ++local) {
+                    const int seg_end = min(seg + kSeg, tb1);
                     const uint32_t buf = local & 1, bphase = (local >> 1) & 1;
                     if (!mbar_wait(bar_tempty + 8 * buf, bphase ^ 1, abort_flag, kWaitLimitNs, kSuspendMmaNs)) {
                         ok = false;
@@ -286,8 +337,7 @@ weight_grad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_const
                     tc_fence_after();
                     const uint32_t d_tmem = tmem_base + buf * BN;
                     for (int tb = seg; tb < seg_end; ++tb) {
-                        if (!mbar_wait(bar_fulla + 8 * stage, phase, abort_flag, kWaitLimitNs, kSuspendMmaNs) ||
-                            !mbar_wait(bar_fullb + 8 * stage, phase, abort_flag, kWaitLimitNs, kSuspendMmaNs)) {
+                        if (!mbar_wait(bar_full + 8 * stage, phase, abort_flag, kWaitLimitNs, kSuspendMmaNs)) {
                             ok = false;
                             break;
                         }
@@ -310,131 +360,12 @@ weight_grad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_const
             while (!mbar_try_wait(bar_drain, 0) && global_timer_ns() - t0 < kWaitLimitNs) {
             }
         }
-    } else if (warp == 2) {
-        // ------------------------------------------------------------ raw code producer (both CTAs)
-        if (lane == 0) {
-            uint32_t stage = 0, phase = 0;
-            uint64_t issued = 0;
-            bool ok = true;
-            for (int item = pair; item < num_items && ok; item += num_pairs) {
-                const int tile = item % tiles, split = item / tiles;
-                const int k0 = (tile % p.num_k) * BN + 128 * int(rank);
-                const int tb0 = split * p.blocks_per_split, tb1 = min(tb0 + p.blocks_per_split, p.num_tb);
-                for (int tb = tb0; tb < tb1; ++tb) {
-                    if (!mbar_wait(bar_rempty + 8 * stage, phase ^ 1, abort_flag, kWaitLimitNs, kSuspendProducerNs)) {
-                        ok = false;
-                        break;
-                    }
-                    mbar_arrive_expect_tx(bar_rfull + 8 * stage, kRawBytes * CB / 8);
-                    tma_load_2d(sbase + kWSmemRaw + stage * kRawBytes, &map_q, k0 * CB / 8, tb * kTokens,
-                                bar_rfull + 8 * stage);
-                    ++issued;
-                    if (++stage == kRawStages) { stage = 0; phase ^= 1; }
-                }
-            }
-            if (!ok) {
-                const uint64_t n = issued < kRawStages ? issued : kRawStages;
-                for (uint64_t i = issued - n; i < issued; ++i) {
-                    const uint32_t st = uint32_t(i % kRawStages), ph = uint32_t((i / kRawStages) & 1);
-                    const uint64_t t0 = global_timer_ns();
-                    while (!mbar_try_wait(bar_rfull + 8 * st, ph) && global_timer_ns() - t0 < kWaitLimitNs) {
-                    }
-                }
-            }
-        }
       }
-    } else if (warp < 12) {
-        // ------------------------------------------------------------ code conversion (warps 4..11, both CTAs)
-        regs_dec<kRegsConv>();
-        const int group = (warp - 4) >> 2, cw = warp & 3;   // the group converts every second block of the pair
-        const int t = (cw & 1) * 32 + lane;    // token of the block
-        const int half = cw >> 1;              // 64-column box of the CTA's 128 columns
-        const uint32_t fullb_even = map_to_rank(bar_fullb, 0);
-        const float2 neg_off = make_float2(-p.offset, -p.offset);
-        uint32_t stage = group, phase = 0, rstage = group, rphase = 0;
-        int done = 0;                          // blocks of the items so far
-        bool ok = true;
-        for (int item = pair; item < num_items && ok; item += num_pairs) {
-            const int tile = item % tiles, split = item / tiles;
-            const int k0 = (tile % p.num_k) * BN + 128 * int(rank);
-            const int tb0 = split * p.blocks_per_split, tb1 = min(tb0 + p.blocks_per_split, p.num_tb);
-            // this token's step, fetched one turn ahead; 0 past the last token or column, where
-            // the codes read as zero too
-            const float* sc = p.scales + (p.scale_stride == 1 ? 0 : k0 / 128);
-            auto step_of = [&](int tb) {
-                const int64_t tok = int64_t(tb) * kTokens + t;
-                return tok < p.T && k0 < p.K && tb < tb1 ? __ldg(sc + tok * p.scale_stride) * p.mul : 0.0f;
-            };
-            int tb = tb0 + ((group ^ done) & 1);
-            done += tb1 - tb0;
-            float next = step_of(tb);
-            for (; tb < tb1; tb += 2) {
-                const float2 step = make_float2(next, next);
-                next = step_of(tb + 2);
-                // (giving up is decided by the whole warp: its lanes meet again below)
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar_rfull + 8 * rstage, rphase, abort_flag, kWaitLimitNs,
-                                                       kSuspendProducerNs)) ||
-                    !__all_sync(0xFFFFFFFFu, mbar_wait(bar_empty + 8 * stage, phase ^ 1, abort_flag, kWaitLimitNs,
-                                                       kSuspendProducerNs))) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t raw = sbase + kWSmemRaw + rstage * kRawBytes;
-                const uint32_t row = sbase + kWSmemB + stage * kWStageB + half * kWBox + t * 128;
-#pragma unroll
-                for (int j = 0; j < CB / 2; ++j) {
-                    const uint32_t at = CB == 8 ? raw + t * 128 + (((half * 4 + j) ^ (t & 7)) << 4)
-                                                : raw + t * 64 + (((half * 2 + j) ^ ((t >> 1) & 3)) << 4);
-                    uint32_t w[4];
-                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                                 : "r"(at)
-                                 : "memory");
-                    if constexpr (CB == 8) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t o[4];
-                            convert4(w[2 * h] ^ p.flip, neg_off, step, o[0], o[1]);
-                            convert4(w[2 * h + 1] ^ p.flip, neg_off, step, o[2], o[3]);
-                            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
-                                             row + (((2 * j + h) ^ (t & 7)) << 4)),
-                                         "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
-                                         : "memory");
-                        }
-                    } else {
-#pragma unroll
-                        for (int h = 0; h < 4; ++h) {
-                            // low nibbles are the even elements, high nibbles the odd ones
-                            const uint32_t u = w[h] ^ p.flip, ev = u & 0x0F0F0F0Fu, od = (u >> 4) & 0x0F0F0F0Fu;
-                            uint32_t o[4];
-                            convert4(__byte_perm(ev, od, 0x5140), neg_off, step, o[0], o[1]);
-                            convert4(__byte_perm(ev, od, 0x7362), neg_off, step, o[2], o[3]);
-                            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
-                                             row + (((4 * j + h) ^ (t & 7)) << 4)),
-                                         "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
-                                         : "memory");
-                        }
-                    }
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    // the raw slot is returned only now that its values have arrived and been used: an arrival
-                    // right behind the loads does not wait for them, and rarely let the next copy overtake one
-                    mbar_arrive(bar_rempty + 8 * rstage);
-                    mbar_arrive_remote(fullb_even + 8 * stage);
-                }
-                rstage += 2;
-                if (rstage >= kRawStages) { rstage -= kRawStages; rphase ^= 1; }
-                stage += 2;
-                if (stage >= kWStages) { stage -= kWStages; phase ^= 1; }
-            }
-        }
     } else {
-        // ------------------------------------------------------------ epilogue teams (warps 12..19, both CTAs)
+        // ------------------------------------------------------------ epilogue teams (warps 4..11, both CTAs)
         regs_inc<kRegsTeam>();
-        const int team = (warp - 12) >> 2;     // 128-column half of the tile
-        const int et = threadIdx.x - 32 * (12 + 4 * team), bar_id = 1 + team;
+        const int team = (warp - 4) >> 2;      // 128-column half of the tile
+        const int et = threadIdx.x - 32 * (4 + 4 * team), bar_id = 1 + team;
         const int quarter = warp & 3;
         const int row_in_tile = quarter * 32 + lane;
         const uint32_t lane_addr = uint32_t(quarter * 32) << 16;
@@ -451,7 +382,7 @@ weight_grad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_const
 #pragma unroll
             for (int i = 0; i < 64; ++i) w[i] = make_float2(0.0f, 0.0f);
 #pragma unroll 1
-            for (int seg = tb0; seg < tb1; seg += kSegBlocks, ++local) {
+            for (int seg = tb0; seg < tb1; seg += kSeg, ++local) {
                 const uint32_t buf = local & 1, bphase = (local >> 1) & 1;
                 const bool got = mbar_wait(bar_tfull + 8 * buf, bphase, abort_flag, kWaitLimitNs, kSuspendEpilogueNs);
                 if (team_any(bar_id, !got)) {
@@ -628,26 +559,42 @@ SplitPlan plan_splits(int64_t T, int64_t N, int64_t K) {
     return s;
 }
 
-template <int CB, int OUT>
+// The workspace: xh [T, K] bf16, then (with token splits) the splits' sums [splits, raw_rows, K] fp32.
+int64_t xh_bytes(int64_t T, int64_t K) { return (T * K * 2 + 255) / 256 * 256; }
+
+template <int CB>
+cudaError_t launch_restore(const WeightGradArgs& a, cudaStream_t stream) {
+    RestoreParams p;
+    p.codes = reinterpret_cast<const uint4*>(a.codes);
+    p.scales = a.scales;
+    p.xh = static_cast<uint4*>(a.workspace);
+    p.per_row = (int)(a.K * CB / 128);
+    p.chunks = a.T * p.per_row;
+    p.scale_shift = a.groups == 1 ? 31 : (CB == 8 ? 3 : 2);   // 128 columns are 8 or 4 chunks
+    p.groups = a.groups;
+    p.offset = 32768.0f + a.offset;
+    p.mul = a.mul;
+    p.flip = CB == 8 ? 0x80808080u : 0x88888888u;
+    const int64_t blocks = (p.chunks + 255) / 256;
+    const int64_t most = int64_t(sm_count()) * max_ctas_per_sm((const void*)restore_codes_kernel<CB>, 256, 0);
+    return launch_pdl(restore_codes_kernel<CB>, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0, stream, p);
+}
+
+template <int OUT>
 cudaError_t launch_main(const WeightGradArgs& a, const SplitPlan& plan, cudaStream_t stream) {
-    CUtensorMap mg, mq, mo;
-    void* dst = OUT == kOutRaw ? a.workspace : a.out;
+    CUtensorMap mg, mx, mo;
+    void* dst = OUT == kOutRaw ? static_cast<char*>(a.workspace) + xh_bytes(a.T, a.K) : a.out;
     const uint64_t rows = OUT == kOutRaw ? uint64_t(plan.splits) * plan.raw_rows : uint64_t(a.N);
     const bool bf = OUT == kOutBf16;
     if (!make_map_2d(&mg, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.gy, a.N, a.T, a.ld_gy * 2, 64, kTokens,
                      CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_map_2d(&mq, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.codes, a.K * CB / 8, a.T, a.K * CB / 8, 128 * CB / 8, kTokens,
-                     CB == 8 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !make_map_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.workspace, a.K, a.T, a.K * 2, 64, kTokens,
+                     CU_TENSOR_MAP_SWIZZLE_128B) ||
         !make_map_2d(&mo, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dst, a.K, rows,
                      a.K * (bf ? 2 : 4), bf ? 32 : 16, 128, CU_TENSOR_MAP_SWIZZLE_64B))
         return cudaErrorInvalidValue;
     WeightGradParams p;
     p.mask = a.mask;
-    p.scales = a.scales;
-    p.scale_stride = a.groups;
-    p.offset = 32768.0f + a.offset;
-    p.mul = a.mul;
-    p.flip = CB == 8 ? 0x80808080u : 0x88888888u;
     p.T = (int)a.T; p.N = (int)a.N; p.K = (int)a.K;
     p.num_n = (int)((a.N + 255) / 256);
     p.num_k = (int)((a.K + BN - 1) / BN);
@@ -660,27 +607,26 @@ cudaError_t launch_main(const WeightGradArgs& a, const SplitPlan& plan, cudaStre
     int dev = 0;
     cudaGetDevice(&dev);
     if (attr_dev != dev) {
-        cudaError_t e = cudaFuncSetAttribute(weight_grad_kernel<CB, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t e = cudaFuncSetAttribute(weight_grad_kernel<OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              kWSmemTotal);
         if (e != cudaSuccess) return e;
         attr_dev = dev;
     }
     const int64_t items = int64_t(p.num_n) * p.num_k * p.splits;
-    const int pairs = pair_clusters(dev, (const void*)weight_grad_kernel<CB, OUT>, kWThreads, kWSmemTotal);
+    const int pairs = pair_clusters(dev, (const void*)weight_grad_kernel<OUT>, kWThreads, kWSmemTotal);
     const int grid_pairs = items < pairs ? (int)items : pairs;
-    return launch_pdl(weight_grad_kernel<CB, OUT>, dim3(2 * grid_pairs), dim3(kWThreads), kWSmemTotal, stream, mg, mq,
+    return launch_pdl(weight_grad_kernel<OUT>, dim3(2 * grid_pairs), dim3(kWThreads), kWSmemTotal, stream, mg, mx,
                       mo, p);
 }
 
-template <int CB>
-cudaError_t launch_bits(const WeightGradArgs& a, const SplitPlan& plan, cudaStream_t stream) {
-    if (plan.splits == 1)
-        return a.out_fp32 ? launch_main<CB, kOutF32>(a, plan, stream) : launch_main<CB, kOutBf16>(a, plan, stream);
-    cudaError_t e = launch_main<CB, kOutRaw>(a, plan, stream);
+cudaError_t launch_product(const WeightGradArgs& a, const SplitPlan& plan, cudaStream_t stream) {
+    if (plan.splits == 1) return a.out_fp32 ? launch_main<kOutF32>(a, plan, stream) : launch_main<kOutBf16>(a, plan, stream);
+    cudaError_t e = launch_main<kOutRaw>(a, plan, stream);
     if (e != cudaSuccess) return e;
     const int64_t blocks = (a.N * (a.K / 128) + 7) / 8;
     const dim3 grid((unsigned)(blocks < 16384 ? blocks : 16384));
-    const float4* part = static_cast<const float4*>(a.workspace);
+    const float4* part =
+        reinterpret_cast<const float4*>(static_cast<const char*>(a.workspace) + xh_bytes(a.T, a.K));
     if (a.out_fp32)
         return launch_pdl(weight_grad_finish_kernel<float>, grid, dim3(256), 0, stream, part, a.mask,
                           static_cast<float*>(a.out), a.N, (int)a.K, plan.splits, plan.raw_rows, a.accumulate);
@@ -693,7 +639,7 @@ cudaError_t launch_bits(const WeightGradArgs& a, const SplitPlan& plan, cudaStre
 size_t weight_grad_workspace_bytes(int64_t T, int64_t N, int64_t K) {
     if (T == 0 || N == 0 || K == 0) return 0;
     const SplitPlan s = plan_splits(T, N, K);
-    return s.splits == 1 ? 0 : size_t(s.splits) * size_t(s.raw_rows) * size_t(K) * 4;
+    return size_t(xh_bytes(T, K)) + (s.splits == 1 ? 0 : size_t(s.splits) * size_t(s.raw_rows) * size_t(K) * 4);
 }
 
 cudaError_t launch_weight_grad(const WeightGradArgs& a, cudaStream_t stream) {
@@ -704,7 +650,8 @@ cudaError_t launch_weight_grad(const WeightGradArgs& a, cudaStream_t stream) {
         return launch_zero_fill(static_cast<uint16_t*>(a.out), nullptr, halves, stream);
     }
     const SplitPlan plan = plan_splits(a.T, a.N, a.K);
-    return a.code_bits == 8 ? launch_bits<8>(a, plan, stream) : launch_bits<4>(a, plan, stream);
+    const cudaError_t e = a.code_bits == 8 ? launch_restore<8>(a, stream) : launch_restore<4>(a, stream);
+    return e != cudaSuccess ? e : launch_product(a, plan, stream);
 }
 
 int read_and_clear_weight_grad_status(cudaStream_t stream, cudaError_t* err) {

@@ -516,8 +516,9 @@ quest_status quest_gated_bwd(const void* grad_h, const int8_t* ckpt_codes, const
  *            must be QUEST_FP32): micro-batches into one master gradient.
  *   workspace, workspace_bytes   at least quest_weight_grad_workspace(T, N, K) bytes, 16-byte
  *            aligned, used until the call's work on the stream is done (two calls that may run at
- *            the same time need one each); NULL where that is 0. With few output tiles the tokens are cut
- *            into pieces whose sums meet there, in a fixed order: results do not vary from run to run.
+ *            the same time need one each). It holds x_hat for the length of the call (2 T K bytes); with
+ *            few output tiles the tokens are cut into pieces whose sums meet there too, in a
+ *            fixed order: results do not vary from run to run.
  * Returns QUEST_OK, QUEST_EINVAL, QUEST_EUNSUPPORTED or QUEST_ECUDA; a bounded wait that
  * gives up is reported by quest_device_status as QUEST_ETIMEOUT.
  */
@@ -526,7 +527,7 @@ quest_status quest_weight_grad(const void* grad_y, int64_t ld_gy, const void* co
                                int64_t N, int64_t K, int had_block, void* grad_w, quest_dtype out_dtype,
                                int accumulate, void* workspace, size_t workspace_bytes, void* stream);
 
-/* Bytes of workspace quest_weight_grad needs on the current device; 0 if none (or if a size is invalid). */
+/* Bytes of workspace quest_weight_grad needs on the current device; 0 if a size is 0 or invalid. */
 size_t quest_weight_grad_workspace(int64_t T, int64_t N, int64_t K);
 
 /*

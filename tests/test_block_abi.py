@@ -18,7 +18,7 @@ def gated_bwd(gh=P[0], codes=P[1], scales=P[2], M=4, F=32, act=0, grad=P[3], h=P
 
 
 def weight_grad(gy=P[0], ld=32, codes=P[1], mode=0, bits=8, scales=P[2], rms=128, mask=P[3], T=4, N=32, K=256, had=128,
-                out=P[4], dt=0, acc=0, ws=None, ws_bytes=0):
+                out=P[4], dt=0, acc=0, ws=P[5], ws_bytes=1 << 24):
     return q.load_library().quest_weight_grad(gy, ld, codes, mode, bits, scales, rms, mask, T, N, K, had, out, dt, acc,
                                               ws, ws_bytes, None)
 
@@ -47,7 +47,8 @@ REFUSED = [
                            dict(acc=1), dict(acc=2, dt=1), dict(gy=None), dict(codes=None), dict(scales=None),
                            dict(out=None), dict(gy=P[0] + 8), dict(codes=P[1] + 4), dict(scales=P[2] + 2),
                            dict(mask=P[3] + 8), dict(out=P[4] + 4), dict(out=P[1] + 128), dict(out=P[3]),
-                           dict(T=1 << 31)]),
+                           dict(T=1 << 31), dict(ws=None), dict(ws_bytes=2047), dict(ws=P[5] + 8), dict(ws=P[0]),
+                           dict(ws=P[4] + 64)]),
     (weight_grad, EUNSUPPORTED, [dict(mode=3, bits=4), dict(mode=4, bits=4), dict(bits=2), dict(bits=1), dict(had=64)]),
     (lowbit_linear, EINVAL, [dict(M=-1), dict(N=12), dict(K=192), dict(K=384, ld=384, had=256), dict(ld=128),
                              dict(ld=260), dict(had=100), dict(had=-1), dict(rms=64), dict(mode=9), dict(x=None),

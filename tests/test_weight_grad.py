@@ -77,7 +77,7 @@ def test_many_tiles(cuda_device, kind):
     T, N, K = 150, 2568, 2176
     gy, mask = grad_and_mask(T, N, K, seed=1)
     codes, scales, xh, bits, mode = saved(T, K, kind, False, seed=2)
-    assert q.weight_grad_workspace(T, N, K) == 0
+    assert q.weight_grad_workspace(T, N, K) < 2 * T * K + 256       # no split sums
     for out in (BF, torch.float32):
         check(q.weight_grad(gy, codes, scales, bits, code_mode=mode, mask=mask, out_dtype=out), gy, xh, mask, T)
     q.device_status()
@@ -86,7 +86,7 @@ def test_many_tiles(cuda_device, kind):
 def test_split_tokens(cuda_device):
     # few output tiles: the tokens are cut; results repeat bit for bit, whatever the workspace held
     T, N, K = 8200, 264, 256
-    assert q.weight_grad_workspace(T, N, K) > 0
+    assert q.weight_grad_workspace(T, N, K) > 2 * T * K + N * K * 8  # two splits' sums at least
     gy, mask = grad_and_mask(T, N, K, seed=3)
     codes, scales, xh, bits, mode = saved(T, K, "int8", False, seed=4)
     one = q.weight_grad(gy, codes, scales, bits, code_mode=mode, mask=mask, out_dtype=torch.float32)
