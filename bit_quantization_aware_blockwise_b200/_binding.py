@@ -53,8 +53,10 @@ SIGNATURES = {
     "quest_weight_grad": (_int, [_p, _i64, _p, _int, _int, _p, _i64, _p, _i64, _i64, _i64, _int, _p, _int, _int, _p,
                                  _sz, _p]),
     "quest_weight_grad_workspace": (_sz, [_i64, _i64, _i64]),
-    "quest_lowbit_linear": (_int, [_p, _i64, _p, _int, _p, _i64, _i64, _i64, _i64, _int, _p, _p]),
-    "quest_lowbit_gated": (_int, [_p, _i64, _p, _p, _p, _p, _int, _i64, _i64, _i64, _i64, _int, _int, _p, _p]),
+    "quest_lowbit_linear": (_int, [_p, _i64, _p, _int, _p, _i64, _i64, _i64, _i64, _int, _p, _p, _sz, _p]),
+    "quest_lowbit_gated": (_int, [_p, _i64, _p, _p, _p, _p, _int, _i64, _i64, _i64, _i64, _int, _int, _p, _p, _sz,
+                                  _p]),
+    "quest_lowbit_workspace": (_sz, [_i64, _i64]),
 }
 
 # The benchmark's tensor-core rate probes (include/quest_probe.h), in their own library.
@@ -211,15 +213,22 @@ def weight_grad_workspace(T: int, N: int, K: int) -> int:
     return int(load_library().quest_weight_grad_workspace(T, N, K))
 
 
-def lowbit_linear_raw(x, ld_x, w_codes, code_mode, w_scales, rms_group, M, N, K, had_block, y, stream=0):
+def lowbit_workspace(M: int, K: int) -> int:
+    """Bytes of workspace lowbit_linear_raw and lowbit_gated_raw need (0: none)."""
+    return int(load_library().quest_lowbit_workspace(M, K))
+
+
+def lowbit_linear_raw(x, ld_x, w_codes, code_mode, w_scales, rms_group, M, N, K, had_block, y, workspace=None,
+                      workspace_bytes=0, stream=0):
     _check(load_library().quest_lowbit_linear(x, ld_x, w_codes, code_mode, w_scales, rms_group, M, N, K, had_block, y,
-                                              stream), "quest_lowbit_linear")
+                                              workspace, workspace_bytes, stream), "quest_lowbit_linear")
 
 
 def lowbit_gated_raw(x, ld_x, gate_codes, gate_scales, up_codes, up_scales, code_mode, rms_group, M, F, K, had_block,
-                     act, h, stream=0):
+                     act, h, workspace=None, workspace_bytes=0, stream=0):
     _check(load_library().quest_lowbit_gated(x, ld_x, gate_codes, gate_scales, up_codes, up_scales, code_mode,
-                                             rms_group, M, F, K, had_block, act, h, stream), "quest_lowbit_gated")
+                                             rms_group, M, F, K, had_block, act, h, workspace, workspace_bytes, stream),
+           "quest_lowbit_gated")
 
 
 def device_status(stream=0):
@@ -733,8 +742,10 @@ def lowbit_linear(x, w_codes, w_scales, code_mode: int = CODES_PACKED, had_block
             out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
         else:
             _dense("out", out, (torch.bfloat16,), dev, (M, N))
+        need = lowbit_workspace(M, K)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
         lowbit_linear_raw(x.data_ptr(), _pitch(x), w_codes.data_ptr(), code_mode, w_scales.data_ptr(), group, M, N, K,
-                          had_block, out.data_ptr(), _stream_handle(stream, dev))
+                          had_block, out.data_ptr(), ws.data_ptr() if need else None, need, _stream_handle(stream, dev))
     return out
 
 
@@ -766,9 +777,11 @@ def lowbit_gated(x, gate_codes, gate_scales, up_codes, up_scales, act="silu", co
             out = torch.empty((M, F), dtype=torch.bfloat16, device=dev)
         else:
             _dense("out", out, (torch.bfloat16,), dev, (M, F))
+        need = lowbit_workspace(M, K)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
         lowbit_gated_raw(x.data_ptr(), _pitch(x), gate_codes.data_ptr(), gate_scales.data_ptr(), up_codes.data_ptr(),
                          up_scales.data_ptr(), code_mode, group, M, F, K, had_block, _act(act), out.data_ptr(),
-                         _stream_handle(stream, dev))
+                         ws.data_ptr() if need else None, need, _stream_handle(stream, dev))
     return out
 
 

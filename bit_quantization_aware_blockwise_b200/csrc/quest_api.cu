@@ -963,7 +963,8 @@ quest_status quest_weight_grad(const void* grad_y, int64_t ld_gy, const void* co
 // Shared by the two low-bit calls (up_codes null with `gated` false).
 static quest_status lowbit(const char* what, bool gated, const void* x, int64_t ld_x, const void* const (&codes)[2],
                            const float* const (&scales)[2], quest_code_mode code_mode, int64_t rms_group, int64_t M,
-                           int64_t N, int64_t K, int had_block, quest_act act, void* y, void* stream) {
+                           int64_t N, int64_t K, int had_block, quest_act act, void* y, void* workspace,
+                           size_t workspace_bytes, void* stream) {
     g_last_error.clear();
     if (M < 0 || N < 0 || K < 0) return fail(QUEST_EINVAL, "M, N (F) and K must be >= 0");
     if (N > kMaxDim) return fail(QUEST_EINVAL, "N (F) must be < 2^31");
@@ -994,6 +995,18 @@ static quest_status lowbit(const char* what, bool gated, const void* x, int64_t 
             }
         }
     }
+    const size_t need = M > 0 && N > 0 ? lowbit_workspace_bytes(M, K) : 0;
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need)
+            return fail(QUEST_EINVAL, "workspace must hold quest_lowbit_workspace(M, K) bytes");
+        if (!aligned(workspace, 16)) return fail(QUEST_EINVAL, "workspace must be 16-byte aligned");
+        bool shared = overlap(workspace, (int64_t)need, y, M * N * 2) ||
+                      overlap(workspace, (int64_t)need, x, ((M - 1) * ld_x + K) * 2);
+        for (int w = 0; w < (gated ? 2 : 1); ++w)
+            shared = shared || overlap(workspace, (int64_t)need, codes[w], N * (K / 2)) ||
+                     overlap(workspace, (int64_t)need, scales[w], N * (K / rms_group) * 4);
+        if (shared) return fail(QUEST_EINVAL, "workspace must not overlap anything");
+    }
     if (take_fault(QUEST_FAULT_LAUNCH)) return injected_launch_failure(what);
     LowbitArgs a = {};
     a.x = static_cast<const uint16_t*>(x);
@@ -1008,6 +1021,7 @@ static quest_status lowbit(const char* what, bool gated, const void* x, int64_t 
     a.fp4 = code_mode == QUEST_CODES_FP4_PACKED;
     a.act = (int)act;
     a.y = static_cast<uint16_t*>(y);
+    a.workspace = need > 0 ? workspace : nullptr;
     cudaError_t e = launch_lowbit(a, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, (std::string(what) + " launch").c_str());
     return QUEST_OK;
@@ -1015,23 +1029,28 @@ static quest_status lowbit(const char* what, bool gated, const void* x, int64_t 
 
 extern "C" {
 
+size_t quest_lowbit_workspace(int64_t M, int64_t K) {
+    if (M < 0 || M > 64 || K < 0 || K > 32768 || K % 128 != 0) return 0;
+    return lowbit_workspace_bytes(M, K);
+}
+
 quest_status quest_lowbit_linear(const void* x, int64_t ld_x, const void* w_codes, quest_code_mode code_mode,
                                  const float* w_scales, int64_t rms_group, int64_t M, int64_t N, int64_t K,
-                                 int had_block, void* y, void* stream) {
+                                 int had_block, void* y, void* workspace, size_t workspace_bytes, void* stream) {
     const void* const codes[2] = {w_codes, nullptr};
     const float* const scales[2] = {w_scales, nullptr};
     return lowbit("quest_lowbit_linear", false, x, ld_x, codes, scales, code_mode, rms_group, M, N, K, had_block,
-                  QUEST_ACT_SILU, y, stream);
+                  QUEST_ACT_SILU, y, workspace, workspace_bytes, stream);
 }
 
 quest_status quest_lowbit_gated(const void* x, int64_t ld_x, const void* gate_codes, const float* gate_scales,
                                 const void* up_codes, const float* up_scales, quest_code_mode code_mode,
                                 int64_t rms_group, int64_t M, int64_t F, int64_t K, int had_block, quest_act act,
-                                void* h, void* stream) {
+                                void* h, void* workspace, size_t workspace_bytes, void* stream) {
     const void* const codes[2] = {gate_codes, up_codes};
     const float* const scales[2] = {gate_scales, up_scales};
     return lowbit("quest_lowbit_gated", true, x, ld_x, codes, scales, code_mode, rms_group, M, F, K, had_block, act, h,
-                  stream);
+                  workspace, workspace_bytes, stream);
 }
 
 quest_status quest_debug_inject_fault(quest_fault fault) {

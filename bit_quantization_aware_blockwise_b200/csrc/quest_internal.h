@@ -186,7 +186,9 @@ struct LowbitArgs {
     int had;                       // 0, 16 .. 256
     int fp4, act;
     uint16_t* y;                   // bf16 [M, N]
+    void* workspace;               // lowbit_workspace_bytes(M, K), null if that is 0
 };
+size_t lowbit_workspace_bytes(int64_t M, int64_t K);
 cudaError_t launch_lowbit(const LowbitArgs& a, cudaStream_t stream);
 
 // Number of SMs and max resident CTAs of `func` per SM on the current device.

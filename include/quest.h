@@ -539,9 +539,11 @@ size_t quest_weight_grad_workspace(int64_t T, int64_t N, int64_t K);
  *     xt = H x / sqrt(had_block) per block      (had_block = 0: x is in the Hadamard domain already)
  *     y[m][n] = sum_k xt[m][k] v[n][k] Delta[n][group of k]             bf16 (RNE)
  * with v = q + 1/2 (QUEST_CODES_PACKED, the 4-bit containers of bits 3 and 4) or the E2M1
- * value (QUEST_CODES_FP4_PACKED). xt is held in fp16 under a power of two per token and
- * 128 columns (relative error 2^-12 of values near the group's largest); sums are fp32. A token that
- * holds an Inf or a NaN gives non-finite results, its own only.
+ * value (QUEST_CODES_FP4_PACKED). xt is rounded once, per token and 128 columns: to 16-bit fixed
+ * point for the midrise codes (off by at most 2^-16 of the group's largest value; a group below 2^-100
+ * counts as zero) and to fp16 under a power of two for E2M1 (2^-12 of each value). A group's sum is
+ * exact (midrise) or fp32, the sum over groups fp32. A token that holds an Inf or a NaN gives
+ * non-finite results, its own only.
  *
  * Arguments
  *   x        device bf16 [M, ld_x], 16-byte aligned, ld_x >= K a multiple of 8.
@@ -552,11 +554,17 @@ size_t quest_weight_grad_workspace(int64_t T, int64_t N, int64_t K);
  *   K        0..32768, a multiple of 128 (of 256 with had_block 256). K == 0 writes zeros.
  *   had_block  0, 16, 32, 64, 128 or 256 (the weight's).
  *   y        device bf16 [M, N], 16-byte aligned; overlaps nothing.
+ *   workspace, workspace_bytes   at least quest_lowbit_workspace(M, K) bytes, 16-byte aligned, used until
+ *            the call's work on the stream is done (two calls that may run at the same time need one
+ *            each); NULL where that is 0. It holds the transformed x of larger calls.
  * Returns QUEST_OK, QUEST_EINVAL, QUEST_EUNSUPPORTED or QUEST_ECUDA.
  */
 quest_status quest_lowbit_linear(const void* x, int64_t ld_x, const void* w_codes, quest_code_mode code_mode,
                                  const float* w_scales, int64_t rms_group, int64_t M, int64_t N, int64_t K,
-                                 int had_block, void* y, void* stream);
+                                 int had_block, void* y, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace quest_lowbit_linear and quest_lowbit_gated need; 0 if none (or if a size is invalid). */
+size_t quest_lowbit_workspace(int64_t M, int64_t K);
 
 /*
  * quest_lowbit_gated -- the gated feed-forward block of a few tokens on 4-bit codes:
@@ -567,7 +575,7 @@ quest_status quest_lowbit_linear(const void* x, int64_t ld_x, const void* w_code
 quest_status quest_lowbit_gated(const void* x, int64_t ld_x, const void* gate_codes, const float* gate_scales,
                                 const void* up_codes, const float* up_scales, quest_code_mode code_mode,
                                 int64_t rms_group, int64_t M, int64_t F, int64_t K, int had_block, quest_act act,
-                                void* h, void* stream);
+                                void* h, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * quest_device_status -- synchronises `stream`, then reports (and clears) the

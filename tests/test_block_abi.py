@@ -23,13 +23,14 @@ def weight_grad(gy=P[0], ld=32, codes=P[1], mode=0, bits=8, scales=P[2], rms=128
                                               ws, ws_bytes, None)
 
 
-def lowbit_linear(x=P[0], ld=256, codes=P[1], mode=0, scales=P[2], rms=128, M=4, N=32, K=256, had=128, y=P[3]):
-    return q.load_library().quest_lowbit_linear(x, ld, codes, mode, scales, rms, M, N, K, had, y, None)
+def lowbit_linear(x=P[0], ld=256, codes=P[1], mode=0, scales=P[2], rms=128, M=4, N=32, K=256, had=128, y=P[3],
+                  ws=P[6], ws_bytes=1 << 24):
+    return q.load_library().quest_lowbit_linear(x, ld, codes, mode, scales, rms, M, N, K, had, y, ws, ws_bytes, None)
 
 
 def lowbit_gated(x=P[0], ld=256, cg=P[1], sg=P[2], cu=P[3], su=P[4], mode=0, rms=128, M=4, F=32, K=256, had=128, act=0,
-                 h=P[5]):
-    return q.load_library().quest_lowbit_gated(x, ld, cg, sg, cu, su, mode, rms, M, F, K, had, act, h, None)
+                 h=P[5], ws=P[6], ws_bytes=1 << 24):
+    return q.load_library().quest_lowbit_gated(x, ld, cg, sg, cu, su, mode, rms, M, F, K, had, act, h, ws, ws_bytes, None)
 
 
 REFUSED = [
@@ -55,6 +56,8 @@ REFUSED = [
                              dict(codes=None), dict(scales=None), dict(y=None), dict(x=P[0] + 8), dict(codes=P[1] + 8),
                              dict(scales=P[2] + 2), dict(y=P[3] + 2), dict(y=P[0]), dict(y=P[1] + 16),
                              dict(y=P[2]), dict(N=1 << 31)]),
+    (lowbit_linear, EINVAL, [dict(M=64, K=4096, ld=4096, **kw) for kw in (
+        dict(ws=None), dict(ws_bytes=1000), dict(ws=P[6] + 8), dict(ws=P[0]), dict(ws=P[1]), dict(ws=P[3]))]),
     (lowbit_linear, EUNSUPPORTED, [dict(M=65), dict(K=32896, ld=32896), dict(mode=1), dict(mode=2), dict(mode=5)]),
     (lowbit_gated, EINVAL, [dict(cu=None), dict(su=None), dict(cu=P[3] + 4), dict(su=P[4] + 2), dict(act=7),
                             dict(h=P[3]), dict(F=4), dict(h=None)]),
@@ -92,6 +95,8 @@ def test_workspace_query():
     assert q.weight_grad_workspace(-1, 8, 128) == 0
     assert q.weight_grad_workspace(64, 12, 128) == 0
     assert q.weight_grad_workspace(0, 8, 128) == 0
+    assert q.lowbit_workspace(1, 2048) == 0 and q.lowbit_workspace(65, 2048) == 0
+    assert q.lowbit_workspace(16, 8192) >= 16 * 8192 * 2
 
 
 def test_wrappers_refuse_host_tensors():

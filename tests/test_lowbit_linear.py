@@ -1,11 +1,11 @@
 """quest_lowbit_linear and quest_lowbit_gated against 64-bit formulas (GPU).
 
-Tolerances. The transformed input is held in fp16 under a power of two, off by at most 2^-11 / 2 =
-2^-12 of each value (and 2^-39 of its group's largest where that value is fp16-subnormal); these K
-independent roundings, weighted, stay within six times their root of squares, 6 * 2^-12 R with R =
-sqrt(sum xt^2 w^2) (fixed seeds). The fp32 sums carry an offset of at most 32 / 0.5 times the smallest
-weight: K/16 MMA steps and the group sums stay below 2^-13 R. The result's bf16 rounding is 2^-8 of the
-value. A gated output adds, through |act'| <= 1.13, the two projections' errors times the other factor.
+Tolerances. The transformed input is rounded once: for E2M1 to fp16, off by at most 2^-12 of each value;
+for midrise codes to fixed point with the group's largest value A at 32767, off by at most A / 65534. These
+K independent roundings, weighted, stay within six times the root of their squares, 6 R with R =
+sqrt(sum e^2 w^2), e the bound of each (fixed seeds). The fp32 sums (per group and over groups) and the fp32
+transform add less than 2^-17 of sqrt(sum xt^2 w^2). The result's bf16 rounding is 2^-8 of the value. A gated
+output adds, through |act'| <= 1.13, the two projections' errors times the other factor.
 """
 import pytest
 import torch
@@ -40,13 +40,18 @@ def mode(grid):
     return q.CODES_PACKED if grid == "int4" else q.CODES_FP4_PACKED
 
 
-def product(x, w, had):
+def product(x, w, had, grid):
     xt = ref.transform(x.double(), had)
-    return xt @ w.t(), (6 * 2 ** -12 + 2 ** -13) * (xt.square() @ w.square().t()).sqrt() + 1e-38
+    if grid == "int4":
+        e = (xt.reshape(xt.shape[0], -1, 128).abs().amax(-1) / 65534).repeat_interleave(128, 1)
+    else:
+        e = xt.abs() * 2 ** -12
+    w2 = w.square().t()
+    return xt @ w.t(), 6 * (e.square() @ w2).sqrt() + 2 ** -17 * (xt.square() @ w2).sqrt() + 1e-38
 
 
-def check_linear(got, x, w, had):
-    want, err = product(x, w, had)
+def check_linear(got, x, w, had, grid="int4"):
+    want, err = product(x, w, had, grid)
     assert ((got.double() - want).abs() <= 2 ** -8 * want.abs() + err).all()
 
 
@@ -59,7 +64,7 @@ def test_matches_formula(cuda_device, M, N, K, had, rows, grid):
     codes, scales, w = weight(N, K, grid, rows, seed=N + K)
     x = activations(M, K, seed=M)
     got = q.lowbit_linear(x, codes, scales, code_mode=mode(grid), had_block=had)
-    check_linear(got, x, w, had)
+    check_linear(got, x, w, had, grid)
 
 
 @pytest.mark.parametrize("grid", ["int4", "fp4"])
@@ -71,8 +76,8 @@ def test_gated_matches_formula(cuda_device, M, F, K, had, act, grid):
     cu, su, wu = weight(F, K, grid, False, seed=2)
     x = activations(M, K, seed=M + F)
     got = q.lowbit_gated(x, cg, sg, cu, su, act=act, code_mode=mode(grid), had_block=had)
-    a, ea = product(x, wg, had)
-    b, eb = product(x, wu, had)
+    a, ea = product(x, wg, had, grid)
+    b, eb = product(x, wu, had, grid)
     v, _ = ref.gate(a, act)
     want = v * b
     tol = (2 ** -8 + 2 ** -16) * want.abs() + 1.13 * ea * (b.abs() + eb) + v.abs() * eb + 1e-38
@@ -90,11 +95,11 @@ def test_quantizer_codes_decode(cuda_device):
     # codes of the library's own quantizer, both grids, per group and per row, against its dequantised weights
     W = (torch.randn(264, 512, device="cuda", generator=gen(5)) * 0.02).to(BF)
     x = activations(6, 512, seed=6)
-    for cm in (q.CODES_PACKED, q.CODES_FP4_PACKED):
+    for cm, grid in ((q.CODES_PACKED, "int4"), (q.CODES_FP4_PACKED, "fp4")):
         for rg in (128, 512):
             qw = q.quantize_fwd(W, 4, rms_group=rg, code_mode=cm, mask_mode=None, dequant="fp32")
             got = q.lowbit_linear(x, qw["codes"], qw["scales"], code_mode=cm)
-            check_linear(got, x, qw["dequant"].double(), 128)
+            check_linear(got, x, qw["dequant"].double(), 128, grid)
 
 
 def test_scale_of_the_input(cuda_device):
@@ -132,7 +137,7 @@ def test_pitched_input_and_rows_behind(cuda_device):
     x = wide[:, 8:8 + K]
     out = torch.full((M + 16, N), 7.0, dtype=BF, device="cuda")
     q.lowbit_linear(x, codes, scales, code_mode=q.CODES_FP4_PACKED, out=out[:M])
-    check_linear(out[:M], x, w, 128)
+    check_linear(out[:M], x, w, 128, "fp4")
     assert (out[M:] == 7).all()
 
 
