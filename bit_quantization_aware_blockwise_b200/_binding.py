@@ -7,6 +7,7 @@ it is missing, or a call fails, ``QuestError`` is raised. There is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -261,15 +262,21 @@ def mask_bytes(rows: int, cols: int, mask_mode: int = MASK_BITS) -> int:
 # torch-tensor wrappers (allocate outputs with torch, pass pointers)
 # ---------------------------------------------------------------------------
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream_handle(stream, device):
-    torch = _torch()
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    return _torch()._C._cuda_getCurrentRawStream(device.index)   # torch.cuda.current_stream(device).cuda_stream, 2 us sooner
 
 
 def _require_cuda(t, name):
@@ -566,21 +573,28 @@ class _on:
     __slots__ = ("ctx",)
 
     def __init__(self, device, stream):
-        torch = _torch()
         if stream is not None:
             if stream.device != device:
                 raise QuestError(f"stream is on {stream.device}, the tensors are on {device}")
-            self.ctx = torch.cuda.stream(stream)
+            self.ctx = _torch().cuda.stream(stream)
         else:
-            self.ctx = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+            self.ctx = _torch().cuda.device(device)
 
     def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
+        self.ctx.__enter__()
 
     def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+        self.ctx.__exit__(*exc)
+
+
+_HERE_ALREADY = contextlib.nullcontext()
+
+
+def _at(device, stream):
+    """The context of a call on ``device``: none where it is the current one and no stream is given."""
+    if stream is None and _torch()._C._cuda_getDevice() == device.index:
+        return _HERE_ALREADY
+    return _on(device, stream)
 
 
 def _act(act) -> int:
@@ -593,18 +607,17 @@ def _act(act) -> int:
 def _dense(name, t, dtypes, device, shape=None, pitched=False):
     """Checks a tensor argument: on ``device``, one of ``dtypes``, contiguous (or, ``pitched``,
     2-D with unit column stride) and, where given, of that shape."""
-    if not t.is_cuda:
-        raise QuestError(f"{name} must be a CUDA tensor (there is no CPU path)")
     if t.device != device:
         raise QuestError(f"{name} is on {t.device}, not on {device}")
     if t.dtype not in dtypes:
         raise QuestError(f"{name} must be one of {', '.join(str(d) for d in dtypes)}, not {t.dtype}")
     if pitched:
-        if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        if t.dim() != 2 or (not t.is_contiguous() and ((t.shape[1] > 1 and t.stride(1) != 1) or
+                                                       (t.shape[0] > 1 and t.stride(0) < t.shape[1]))):
             raise QuestError(f"{name} must be 2-D with unit column stride and rows that do not overlap")
     elif not t.is_contiguous():
         raise QuestError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise QuestError(f"{name} must be {list(shape)}, not {list(t.shape)}")
 
 
@@ -635,7 +648,7 @@ def gated_linear(x_hat, w_gate, w_up, act="silu", checkpoint: bool = False, out=
     _dense("x_hat", x_hat, bf, dev)
     _dense("w_gate", w_gate, bf, dev, (F, K))
     _dense("w_up", w_up, bf, dev, (F, K))
-    with _on(dev, stream):
+    with _at(dev, stream):
         if out is None:
             out = torch.empty((M, F), dtype=torch.bfloat16, device=dev)
         else:
@@ -664,7 +677,7 @@ def gated_bwd(grad_h, checkpoint, act="silu", recompute_h: bool = False, out=Non
     codes, scales = checkpoint["codes"], checkpoint["scales"]
     _dense("checkpoint codes", codes, (torch.int8,), dev, (M, 2 * F))
     _dense("checkpoint scales", scales, (torch.float32,), dev, (M, 2 * ((F + 127) // 128)))
-    with _on(dev, stream):
+    with _at(dev, stream):
         if out is None:
             out = torch.empty((M, 2 * F), dtype=torch.bfloat16, device=dev)
         else:
@@ -710,7 +723,7 @@ def weight_grad(grad_y, codes, scales, bits: int, code_mode: int = CODES_PACKED,
     dtype = out_dtype if out_dtype is not None else (out.dtype if out is not None else torch.bfloat16)
     if dtype not in (torch.bfloat16, torch.float32):
         raise QuestError("out_dtype must be bfloat16 or float32")
-    with _on(dev, stream):
+    with _at(dev, stream):
         if out is None:
             out = torch.empty((N, K), dtype=dtype, device=dev)
         else:
@@ -737,7 +750,7 @@ def lowbit_linear(x, w_codes, w_scales, code_mode: int = CODES_PACKED, had_block
     N = w_scales.shape[0]
     _lowbit_weight("w", w_codes, w_scales, N, K, dev)
     group = _rms_group("w_scales", w_scales, N, K) if N > 0 else K
-    with _on(dev, stream):
+    with _at(dev, stream):
         if out is None:
             out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
         else:
@@ -772,7 +785,7 @@ def lowbit_gated(x, gate_codes, gate_scales, up_codes, up_scales, act="silu", co
     group = _rms_group("gate_scales", gate_scales, F, K) if F > 0 else K
     if F > 0 and _rms_group("up_scales", up_scales, F, K) != group:
         raise QuestError("gate_scales and up_scales must have one form")
-    with _on(dev, stream):
+    with _at(dev, stream):
         if out is None:
             out = torch.empty((M, F), dtype=torch.bfloat16, device=dev)
         else:

@@ -55,7 +55,8 @@ namespace {
 constexpr int kGroup = 128;
 constexpr int kMaxCluster = 8;
 constexpr int kChunk = 8;    // groups whose scales are fetched together
-constexpr int kWarps = 16;   // one CTA an SM: x is transformed once per CTA
+constexpr int kWarps = 16;   // one CTA an SM: x's slice is held once
+static_assert((kWarps & (kWarps - 1)) == 0, "the warps along K must divide a CTA's warps: a row group's barrier counts them");
 
 struct LowbitParams {
     const __nv_bfloat16* x;
@@ -292,12 +293,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1) lowbit_kernel(const LowbitPara
     const int g0 = int(rank) * p.slice, ng = max(min(p.slice, p.groups - g0), 0);
     const int wr = kWarps / p.wk, wrow = warp / p.wk, wkk = warp % p.wk;
     // shared memory: B fragments [slice][tokens][256], meta [slice][TOK], the warps' scales [kWarps][2][MATS][16 rows]
-    // [kChunk], the warps' sums [2][kWarps][tile], and with a cluster this CTA's sums [iters * wr][tile]
+    // [kChunk], the warps' sums [kWarps][tile], and with a cluster this CTA's sums [iters * wr][tile]
     uint8_t* frags = lsmem;
     float2* meta = reinterpret_cast<float2*>(lsmem + size_t(p.slice) * tokens * 256);
     float* scales = reinterpret_cast<float*>(meta + p.slice * TOK) + warp * (2 * MATS * 16 * kChunk);
     float* part = reinterpret_cast<float*>(meta + p.slice * TOK) + kWarps * (2 * MATS * 16 * kChunk);
-    float* hold = part + 2 * kWarps * kTile;
+    float* hold = part + kWarps * kTile;
 
     // stage_kernel, if there is one, lets this grid start only after it has itself waited for all earlier work, so the
     // weights may be read while it runs; x's fragments (and y) wait for its end
@@ -514,7 +515,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) lowbit_kernel(const LowbitPara
             }
         }
         // the tile's sums
-        float* dst = part + ((it & 1) * kWarps + warp) * kTile + lg;
+        float* dst = part + warp * kTile + lg;
 #pragma unroll
         for (int w = 0; w < MATS; ++w)
 #pragma unroll
@@ -526,12 +527,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1) lowbit_kernel(const LowbitPara
                     dst[(w * TOK + nt * 8 + 2 * lt + (e & 1)) * 16 + 8 * (e >> 1)] = t;
                     total[w][0][nt][e] = total[w][1][nt][e] = 0.0f;
                 }
-        // the tile's wk warps (the two buffers make one barrier a tile enough)
-        if (p.wk > 1)
-            asm volatile("bar.sync %0, %1;" ::"r"(1 + wrow), "r"(32 * p.wk) : "memory");
-        else
-            __syncwarp();
-        const float* src = part + ((it & 1) * kWarps + wrow * p.wk) * kTile;
+        // the tile's wk warps: all sums written, and below all read before the next tile's
+        auto meet = [&]() {
+            if (p.wk > 1)
+                asm volatile("bar.sync %0, %1;" ::"r"(1 + wrow), "r"(32 * p.wk) : "memory");
+            else
+                __syncwarp();
+        };
+        meet();
+        const float* src = part + wrow * p.wk * kTile;
         for (int i = wkk * 32 + lane; i < 16 * tokens; i += 32 * p.wk) {
             float v[MATS] = {};
             for (int k = 0; k < p.wk; ++k)
@@ -546,6 +550,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) lowbit_kernel(const LowbitPara
                 p.y[int64_t(m0 + (i >> 4)) * p.N + row0 + (i & 15)] = __float2bfloat16_rn(out);
             }
         }
+        meet();
     }
     if (cs == 1) return;
 
@@ -651,7 +656,7 @@ cudaError_t launch_one(const LowbitArgs& a, cudaStream_t stream) {
         const int slice = slice_of(c);
         if (c > 1 && slice == slice_of(c / 2)) break;
         const size_t fixed = size_t(slice) * (tokens * 256 + TOK * 8) + kWarps * (2 * MATS * 16 * kChunk * 4) +
-                             2 * kWarps * kTileBytes;
+                             kWarps * kTileBytes;
         if (fixed > kRoom) continue;
         attr[1].val.clusterDim.x = c;
         cfg.gridDim = dim3((unsigned)c);
