@@ -293,12 +293,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1) lowbit_kernel(const LowbitPara
     const int g0 = int(rank) * p.slice, ng = max(min(p.slice, p.groups - g0), 0);
     const int wr = kWarps / p.wk, wrow = warp / p.wk, wkk = warp % p.wk;
     // shared memory: B fragments [slice][tokens][256], meta [slice][TOK], the warps' scales [kWarps][2][MATS][16 rows]
-    // [kChunk], the warps' sums [kWarps][tile], and with a cluster this CTA's sums [iters * wr][tile]
+    // [kChunk], the warps' sums [kWarps][tile] (if they are to be added), and with a cluster this CTA's sums
+    // [iters * wr][tile]
     uint8_t* frags = lsmem;
     float2* meta = reinterpret_cast<float2*>(lsmem + size_t(p.slice) * tokens * 256);
     float* scales = reinterpret_cast<float*>(meta + p.slice * TOK) + warp * (2 * MATS * 16 * kChunk);
     float* part = reinterpret_cast<float*>(meta + p.slice * TOK) + kWarps * (2 * MATS * 16 * kChunk);
-    float* hold = part + kWarps * kTile;
+    const bool direct = p.wk == 1 && cs > 1;   // a warp's sums are the CTA's
+    float* hold = direct ? part : part + kWarps * kTile;
 
     // stage_kernel, if there is one, lets this grid start only after it has itself waited for all earlier work, so the
     // weights may be read while it runs; x's fragments (and y) wait for its end
@@ -515,7 +517,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) lowbit_kernel(const LowbitPara
             }
         }
         // the tile's sums
-        float* dst = part + warp * kTile + lg;
+        float* dst = (direct ? hold + (it * wr + wrow) * kTile : part + warp * kTile) + lg;
 #pragma unroll
         for (int w = 0; w < MATS; ++w)
 #pragma unroll
@@ -527,6 +529,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) lowbit_kernel(const LowbitPara
                     dst[(w * TOK + nt * 8 + 2 * lt + (e & 1)) * 16 + 8 * (e >> 1)] = t;
                     total[w][0][nt][e] = total[w][1][nt][e] = 0.0f;
                 }
+        if (direct) continue;
         // the tile's wk warps: all sums written, and below all read before the next tile's
         auto meet = [&]() {
             if (p.wk > 1)
@@ -655,8 +658,7 @@ cudaError_t launch_one(const LowbitArgs& a, cudaStream_t stream) {
     for (int c = 1; c <= kMaxCluster; c *= 2) {
         const int slice = slice_of(c);
         if (c > 1 && slice == slice_of(c / 2)) break;
-        const size_t fixed = size_t(slice) * (tokens * 256 + TOK * 8) + kWarps * (2 * MATS * 16 * kChunk * 4) +
-                             kWarps * kTileBytes;
+        const size_t fixed = size_t(slice) * (tokens * 256 + TOK * 8) + kWarps * (2 * MATS * 16 * kChunk * 4);
         if (fixed > kRoom) continue;
         attr[1].val.clusterDim.x = c;
         cfg.gridDim = dim3((unsigned)c);
@@ -667,9 +669,10 @@ cudaError_t launch_one(const LowbitArgs& a, cudaStream_t stream) {
             const int side = kWarps / wk;
             const int64_t turns = (tiles + side - 1) / side;
             int64_t iters = (turns + wave - 1) / wave;
-            size_t need = fixed;
+            size_t need = fixed + (c > 1 && wk == 1 ? 0 : kWarps * kTileBytes);
+            if (need > kRoom) continue;
             if (c > 1) {   // (a long walk over the tiles is cut where their sums fill shared memory)
-                const int64_t most = int64_t((kRoom - fixed) / (side * kTileBytes));
+                const int64_t most = int64_t((kRoom - need) / (side * kTileBytes));
                 if (most < 1) continue;
                 if (iters > most) iters = most;
                 need += size_t(iters) * side * kTileBytes;
