@@ -28,9 +28,8 @@ namespace {
 // per KB of codes, 76 instructions of the integer pipe and 18 MMAs, so the decoding decides the form:
 //
 // Midrise codes stay integers. Flipping a nibble's top bit gives u = q + 8 in 0..15; a word of eight codes
-// becomes two fragment words of bytes with three instructions (fp16 pairs took eight: 461 instructions
-// per KB pair of the gated form in all, 90 us where this one takes what its table entry says). x is rounded to 16-bit fixed
-// point under a scale per token and group, x = 256 hi + lo, and two m16n8k32 integer MMAs give
+// becomes two fragment words of bytes with three instructions (as fp16 pairs it took eight). x is rounded to
+// 16-bit fixed point under a scale per token and group, x = 256 hi + lo, and two m16n8k32 integer MMAs give
 // sum(u hi) and sum(u lo) exactly; sum((q + 1/2) x) = sum(u x) - 7.5 sum(x) is exact too. The rounding of x is
 // the only one before the scales: 2^-16 of the group's largest value.
 //
@@ -41,7 +40,8 @@ namespace {
 // Columns may be permuted freely as long as both operands agree: lane (g, t) of a warp takes the 32
 // codes 32t .. 32t+31 of a 128-column group of rows g and g + 8, and x's fragments are laid out to match.
 // A group of a row is 64 bytes, half a line, and a load instruction whose lanes touch half lines of eight rows
-// leaves the SM waiting on its requests (58 us for the loads alone where whole lines take half). So groups
+// leaves the SM waiting on its requests (the loads alone, with scales: 54 us at 22016 x 8192 twice, 45 with whole
+// lines, 35 once the scales went through shared memory; all of it 90 us and 54). So groups
 // are loaded in pairs: an instruction takes the whole line of four rows, even lanes' rows the first
 // group and odd lanes' rows the second, another instruction the neighbouring rows the other way round, and a
 // select by the lane's parity sorts them. The second group's rows come out pairwise swapped; its sums
@@ -54,6 +54,7 @@ namespace {
 // waits for a tile's end. Partial sums meet in shared memory and are added in warp and rank order.
 constexpr int kGroup = 128;
 constexpr int kMaxCluster = 8;
+constexpr int kLowbitMaxK = 32768;   // as the callers check
 constexpr int kChunk = 8;    // groups whose scales are fetched together
 constexpr int kWarps = 16;   // one CTA an SM: x's slice is held once
 static_assert((kWarps & (kWarps - 1)) == 0, "the warps along K must divide a CTA's warps: a row group's barrier counts them");
@@ -70,7 +71,6 @@ struct LowbitParams {
     int scale_groups;    // scales per row: groups or 1
     int slice;           // groups per CTA of the cluster (even, but for a single CTA's last)
     int wk;              // warps along K
-    int per_warp;        // pairs of groups per warp
     int iters;           // row tiles per warp
     int clusters;
     float had_scale;     // 1 / sqrt(had)
@@ -205,7 +205,7 @@ __device__ __forceinline__ void stage_x(const LowbitParams& p, int m0, int token
             const float amax = __uint_as_float(top);
             const bool zero = amax < 7.888609052210118e-31f;
             const float mul = zero ? 0.0f : __fdividef(32767.0f, amax);
-            int sum = 0;
+            uint32_t sum = 0;   // (two's complement; a non-finite group's wraps)
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
                 uint32_t b[8];
@@ -215,7 +215,7 @@ __device__ __forceinline__ void stage_x(const LowbitParams& p, int m0, int token
                     const float2 f = __ffma2_rn(v[4 * w + j], make_float2(mul, mul), make_float2(12582912.0f, 12582912.0f));
                     b[2 * j] = __float_as_uint(f.x);
                     b[2 * j + 1] = __float_as_uint(f.y);
-                    sum += int(b[2 * j]) + int(b[2 * j + 1]) - 2 * 0x4B400000;
+                    sum += b[2 * j] + b[2 * j + 1] - 2 * 0x4B400000u;
                 }
                 // columns 0 2 4 6 and 1 3 5 7: high bytes, then low bytes
                 out[w] = make_uint4(__byte_perm(__byte_perm(b[0], b[2], 0x0051), __byte_perm(b[4], b[6], 0x0051), 0x5410),
@@ -226,7 +226,7 @@ __device__ __forceinline__ void stage_x(const LowbitParams& p, int m0, int token
 #pragma unroll
             for (int h = 1; h < 8; h <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, h);
             // 15 sum(x), and half the step of x (a non-finite largest value makes it non-finite)
-            entry = make_float2(__int_as_float(15 * sum), zero ? 0.0f : amax * p.had_scale * (0.5f / 32767.0f));
+            entry = make_float2(__uint_as_float(15u * sum), zero ? 0.0f : amax * p.had_scale * (0.5f / 32767.0f));
         }
         if (!live) continue;
 #pragma unroll
@@ -308,10 +308,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) lowbit_kernel(const LowbitPara
 
     const int lg = lane >> 2, lt = lane & 3;
     const bool odd = lg & 1;
-    const int ga = 2 * wkk * p.per_warp;                              // this warp's groups of the slice
-    const int n = max(min(2 * p.per_warp, ng - ga), 0), pairs = (n + 1) / 2;
+    // This warp's pairs of groups of the slice: wkk, wkk + wk, .. (the warps of a tile read along its rows together)
+    const int all_pairs = (ng + 1) / 2, pairs = max((all_pairs - wkk + p.wk - 1) / p.wk, 0);
     const int padded = max((pairs + kPairs - 1) / kPairs, 1) * kPairs;   // whole turns, so that a slot's place is fixed
-    const bool ragged = n & 1;                                        // the last pair has one group
+    const bool ragged = (ng & 1) && pairs > 0 && (all_pairs - 1) % p.wk == wkk;   // the last pair has one group
     auto first_row = [&](int it) { return ((int64_t(it) * p.clusters + cluster) * wr + wrow) * 16; };
     // The next load: tile step, pair there, and the lane's first code line (row lg rounded down to even,
     // group lg & 1) of each matrix; distances to its other lines.
@@ -324,10 +324,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) lowbit_kernel(const LowbitPara
     int to_8 = 0;                                       // rows 8 to 15, if the tile has them (else row lg again)
     auto enter = [&]() {
         const int64_t row = first_row(l_it);
-        l_live = l_it < p.iters && n > 0 && row < p.N;
+        l_live = l_it < p.iters && row < p.N;
         if (!l_live) return;
         to_8 = row + 8 < p.N ? 8 * row_bytes : 0;
-        const int64_t at = (row + (lg & ~1)) * row_bytes + (g0 + ga + int(odd)) * 64 + lt * 16;
+        const int64_t at = (row + (lg & ~1)) * row_bytes + (g0 + 2 * wkk + int(odd)) * 64 + lt * 16;
 #pragma unroll
         for (int w = 0; w < MATS; ++w) l_code[w] = p.codes[w] + at;
     };
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) lowbit_kernel(const LowbitPara
             qd[1] = __ldcs(reinterpret_cast<const uint4*>(c1));
             qd[2] = __ldcs(reinterpret_cast<const uint4*>(c + to_8));
             qd[3] = __ldcs(reinterpret_cast<const uint4*>(c1 + to_8));
-            l_code[mat] += 128;
+            l_code[mat] += p.wk * 128;
         }
         if (mat == MATS - 1) {
             ++l_pair;
@@ -359,10 +359,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) lowbit_kernel(const LowbitPara
     const bool by_row = p.scale_groups == 1;
     const bool wide = (p.scale_groups & 1) == 0 && ((reinterpret_cast<uintptr_t>(p.scales[0]) |
                                                      reinterpret_cast<uintptr_t>(p.scales[MATS - 1])) & 7) == 0;
-    int s_it = 0, s_at = 0, s_buf = 0;        // the next chunk: tile step, first group of the warp's, buffer
+    int s_it = 0, s_at = 0, s_buf = 0;        // the next chunk: tile step, first of the warp's groups, buffer
     auto fetch_scales = [&]() {
         const int64_t row0 = first_row(s_it);
-        if (s_it < p.iters && row0 < p.N && n > 0) {
+        if (s_it < p.iters && row0 < p.N && pairs > 0) {
             float* dst = scales + s_buf * (MATS * 16 * kChunk);
 #pragma unroll
             for (int w = 0; w < MATS; ++w) {
@@ -373,22 +373,26 @@ __global__ void __launch_bounds__(kWarps * 32, 1) lowbit_kernel(const LowbitPara
 #pragma unroll
                     for (int i = 0; i < 16 * kChunk / 64; ++i) {
                         const int at = 2 * (lane + 32 * i), r = at / kChunk, g = at % kChunk;
-                        if (s_at + g < n)
-                            copy_async<8>(dst + w * 16 * kChunk + at, p.scales[w] + min(row0 + r, int64_t(p.N) - 1) * p.scale_groups + g0 + ga + s_at + g);
+                        const int group = 2 * (wkk + (s_at + g) / 2 * p.wk) + (g & 1);
+                        if (group < ng)
+                            copy_async<8>(dst + w * 16 * kChunk + at,
+                                          p.scales[w] + min(row0 + r, int64_t(p.N) - 1) * p.scale_groups + g0 + group);
                     }
                 } else {
 #pragma unroll
                     for (int i = 0; i < 16 * kChunk / 32; ++i) {
                         const int at = lane + 32 * i, r = at / kChunk, g = at % kChunk;
-                        if (s_at + g < n)
-                            copy_async<4>(dst + w * 16 * kChunk + at, p.scales[w] + min(row0 + r, int64_t(p.N) - 1) * p.scale_groups + g0 + ga + s_at + g);
+                        const int group = 2 * (wkk + (s_at + g) / 2 * p.wk) + (g & 1);
+                        if (group < ng)
+                            copy_async<4>(dst + w * 16 * kChunk + at,
+                                          p.scales[w] + min(row0 + r, int64_t(p.N) - 1) * p.scale_groups + g0 + group);
                     }
                 }
             }
         }
         s_buf ^= 1;
         s_at += kChunk;
-        if (by_row || s_at >= n) {
+        if (by_row || s_at >= 2 * pairs) {
             s_at = 0;
             ++s_it;
         }
@@ -419,9 +423,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) lowbit_kernel(const LowbitPara
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int bm = min(nt * 8 + lg, tokens - 1);
-        frag0[nt] = uint32_t(ga * tokens + bm) * 256 + ((bm & 3) << 6) + lt * 16;   // (from `frags`)
+        frag0[nt] = uint32_t(2 * wkk * tokens + bm) * 256 + ((bm & 3) << 6) + lt * 16;   // (from `frags`)
     }
-    const uint32_t meta0 = uint32_t(p.slice) * tokens * 256 + uint32_t(ga * TOK + 2 * lt) * 8;
+    const uint32_t meta0 = uint32_t(p.slice) * tokens * 256 + uint32_t(2 * wkk * TOK + 2 * lt) * 8;
     float total[MATS][2][NT][4] = {};        // [matrix][group of the pair]
     int c_buf = 0;                           // the scales' buffer in use
 
@@ -469,7 +473,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) lowbit_kernel(const LowbitPara
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     // 2 (256 hi + lo) - 15 sum(x), below 2^28 in magnitude
-                    const int v = 512 * hi[nt][e] + (2 * lo[nt][e] - int(e & 1 ? mm.z : mm.x));
+                    const int v = int(uint32_t(512 * hi[nt][e] + 2 * lo[nt][e]) - (e & 1 ? mm.z : mm.x));
                     tot[nt][e] = fmaf((e < 2 ? s0 : s1) * __uint_as_float(e & 1 ? mm.w : mm.y), __int2float_rn(v), tot[nt][e]);
                 }
             }
@@ -512,8 +516,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) lowbit_kernel(const LowbitPara
                     }
                     load(qd, w, d == kPairs - 1);
                 }
-                frag_at += tokens * 512;
-                meta_at += TOK * 16;
+                frag_at += p.wk * tokens * 512;
+                meta_at += p.wk * TOK * 16;
             }
         }
         // the tile's sums
@@ -652,6 +656,9 @@ cudaError_t launch_one(const LowbitArgs& a, cudaStream_t stream) {
     // over the cluster). Larger clusters leave SMs empty (their CTAs share a GPC), so the clusters that run at once are asked
     // of the runtime. Shared memory must hold the slice of x, the warps' sums and, in a cluster, every tile's sums.
     constexpr size_t kRoom = 226 * 1024;
+    static_assert(kLowbitMaxK / kGroup / kMaxCluster * (TOK * 256 + TOK * 8) + kWarps * (2 * MATS * 16 * kChunk * 4) +
+                          kWarps * kTileBytes + kTileBytes <= kRoom,
+                  "the longest rows fit with the largest cluster and all warps along K");
     int cs = 0;
     int64_t best = 0, clusters = 0;
     size_t smem = 0;
@@ -686,13 +693,11 @@ cudaError_t launch_one(const LowbitArgs& a, cudaStream_t stream) {
                 clusters = used;
                 smem = need;
                 p.wk = wk;
-                p.per_warp = per_warp;
                 p.slice = slice;
                 p.iters = (int)iters;
             }
         }
     }
-    if (cs == 0) return cudaErrorInvalidConfiguration;
     p.clusters = (int)clusters;
     if (p.staged) {
         const dim3 grid((unsigned)((p.groups * tokens + 15) / 16), (unsigned)token_tiles);
@@ -707,12 +712,7 @@ cudaError_t launch_one(const LowbitArgs& a, cudaStream_t stream) {
 
 template <bool FP4, bool GATED, int ACT>
 cudaError_t launch_tokens(const LowbitArgs& a, cudaStream_t stream) {
-    // 16 tokens at a time, unless they and the longest rows do not fit in shared memory together
-    if (a.M > 8) {
-        const cudaError_t e = launch_one<FP4, 2, GATED, ACT>(a, stream);
-        if (e != cudaErrorInvalidConfiguration) return e;
-    }
-    return launch_one<FP4, 1, GATED, ACT>(a, stream);
+    return a.M <= 8 ? launch_one<FP4, 1, GATED, ACT>(a, stream) : launch_one<FP4, 2, GATED, ACT>(a, stream);
 }
 
 template <bool FP4>

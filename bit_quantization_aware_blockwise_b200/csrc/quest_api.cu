@@ -905,7 +905,7 @@ quest_status quest_weight_grad(const void* grad_y, int64_t ld_gy, const void* co
     if (had_block != 128) return fail(QUEST_EUNSUPPORTED, "quest_weight_grad: had_block must be 128");
     if (K % 128 != 0) return fail(QUEST_EINVAL, "K must be a multiple of 128");
     if (N % 8 != 0) return fail(QUEST_EINVAL, "N must be a multiple of 8 (16-byte rows)");
-    if (ld_gy < N || ld_gy % 8 != 0) return fail(QUEST_EINVAL, "ld_gy must be >= N and a multiple of 8");
+    if (ld_gy < N || ld_gy % 8 != 0 || ld_gy > kMaxDim) return fail(QUEST_EINVAL, "ld_gy must be >= N, a multiple of 8 and < 2^31");
     if (rms_group != 128 && rms_group != K) return fail(QUEST_EINVAL, "rms_group must be 128 or K");
     if (out_dtype != QUEST_BF16 && out_dtype != QUEST_FP32) return fail(QUEST_EINVAL, "invalid out_dtype");
     if (accumulate != 0 && accumulate != 1) return fail(QUEST_EINVAL, "accumulate must be 0 or 1");
@@ -977,7 +977,7 @@ static quest_status lowbit(const char* what, bool gated, const void* x, int64_t 
     if (K % 128 != 0 || (had_block == 256 && K % 256 != 0))
         return fail(QUEST_EINVAL, "K must be a multiple of 128 and of had_block");
     if (N % 8 != 0) return fail(QUEST_EINVAL, "N (F) must be a multiple of 8");
-    if (ld_x < K || ld_x % 8 != 0) return fail(QUEST_EINVAL, "ld_x must be >= K and a multiple of 8");
+    if (ld_x < K || ld_x % 8 != 0 || ld_x > kMaxDim) return fail(QUEST_EINVAL, "ld_x must be >= K, a multiple of 8 and < 2^31");
     if (rms_group != 128 && rms_group != K) return fail(QUEST_EINVAL, "rms_group must be 128 or K");
     if (gated && !valid_act(act)) return fail(QUEST_EINVAL, "invalid act");
     if (M > 0 && N > 0) {

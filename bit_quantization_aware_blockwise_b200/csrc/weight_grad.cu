@@ -23,8 +23,8 @@ namespace {
 //   gw[n][b] = H (mask[n][b] * G[n][b]) / sqrt(128)   per 128-column block b of a row
 //
 // Two launches. A streaming pass restores xh into the workspace (byte -> fp32 by a byte permute
-// onto 2^15, minus the offset, times the token's step, rounded to bf16 as the quantizer's dequant
-// is): 3 bytes moved per value. The product then runs at the tensor cores' rate. Restoring inside
+// onto 2^15, minus the offset, times the token's step, rounded to bf16, as the quantizer's dequant is but for
+// rare ties): 3 bytes moved per value. The product then runs at the tensor cores' rate. Restoring inside
 // the product's mainloop instead repeats the work for every 256 rows of G: eight conversion warps
 // beside the MMAs took 694 us at 16384 x 11264 x 2048, of which 190 us went away with the
 // conversion's arithmetic and stores taken out; the pass costs about 20.

@@ -492,8 +492,9 @@ quest_status quest_gated_bwd(const void* grad_h, const int8_t* ckpt_codes, const
  * its input, with the trust backward fused into the product.
  *
  * The layer's input need not be kept in bf16 between the passes: its codes (8 or 4 bits a
- * value) and steps stand for the very operand the forward multiplied,
- *     x_hat  = bf16( (q + 1/2) Delta )                      (quest_quantize_fwd's dequant)
+ * value) and steps stand for the operand the forward multiplied,
+ *     x_hat  = bf16( (q + 1/2) Delta )      (quest_quantize_fwd's bf16 dequant, but for one bf16
+ *                                            step in about a value of 10^4, next to a tie)
  *     G      = grad_y^T x_hat                 [N, K]        (fp32 accumulation)
  *     grad_w = H (m * G) / sqrt(128) per 128-column block
  * (pith.science review, "What carries the argument" and Figure 2 caption, as for

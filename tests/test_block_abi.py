@@ -43,7 +43,7 @@ REFUSED = [
                          dict(grad=None), dict(gh=P[0] + 2), dict(codes=P[1] + 8), dict(scales=P[2] + 1),
                          dict(grad=P[3] + 8), dict(h=P[4] + 4), dict(grad=P[0]), dict(h=P[0] + 16), dict(h=P[3] + 32),
                          dict(M=1 << 31)]),
-    (weight_grad, EINVAL, [dict(T=-1), dict(N=-8), dict(K=-128), dict(N=12), dict(K=200), dict(ld=24), dict(ld=36),
+    (weight_grad, EINVAL, [dict(T=-1), dict(N=-8), dict(K=-128), dict(N=12), dict(K=200), dict(ld=24), dict(ld=36), dict(ld=1 << 40),
                            dict(bits=0), dict(bits=9), dict(mode=6), dict(had=100), dict(rms=64), dict(dt=2),
                            dict(acc=1), dict(acc=2, dt=1), dict(gy=None), dict(codes=None), dict(scales=None),
                            dict(out=None), dict(gy=P[0] + 8), dict(codes=P[1] + 4), dict(scales=P[2] + 2),
@@ -52,7 +52,7 @@ REFUSED = [
                            dict(ws=P[4] + 64)]),
     (weight_grad, EUNSUPPORTED, [dict(mode=3, bits=4), dict(mode=4, bits=4), dict(bits=2), dict(bits=1), dict(had=64)]),
     (lowbit_linear, EINVAL, [dict(M=-1), dict(N=12), dict(K=192), dict(K=384, ld=384, had=256), dict(ld=128),
-                             dict(ld=260), dict(had=100), dict(had=-1), dict(rms=64), dict(mode=9), dict(x=None),
+                             dict(ld=260), dict(ld=1 << 40), dict(had=100), dict(had=-1), dict(rms=64), dict(mode=9), dict(x=None),
                              dict(codes=None), dict(scales=None), dict(y=None), dict(x=P[0] + 8), dict(codes=P[1] + 8),
                              dict(scales=P[2] + 2), dict(y=P[3] + 2), dict(y=P[0]), dict(y=P[1] + 16),
                              dict(y=P[2]), dict(N=1 << 31)]),

@@ -150,23 +150,79 @@ def test_empty_sizes(cuda_device):
     assert q.lowbit_linear(torch.zeros((0, 128), dtype=BF, device="cuda"), codes, scales).shape == (0, 8)
 
 
-def test_streams_graphs_and_repeats(cuda_device):
+@pytest.mark.parametrize("M,grid", [(1, "int4"), (4, "int4"), (16, "int4"), (40, "fp4")])
+def test_streams_graphs_and_repeats(cuda_device, M, grid):
+    # with 16 and 40 tokens x is transformed by a kernel of its own, through a workspace
     N, K = 1032, 2048
-    codes, scales, w = weight(N, K, "int4", False, seed=14)
-    x, x2 = activations(4, K, seed=15), activations(4, K, seed=16)
-    want, want2 = (q.lowbit_gated(v, codes, scales, codes, scales) for v in (x, x2))
+    assert (q.lowbit_workspace(M, K) > 0) == (M >= 16)
+    codes, scales, w = weight(N, K, grid, False, seed=14)
+    x, x2 = activations(M, K, seed=15), activations(M, K, seed=16)
+
+    def call(v, **kw):
+        return q.lowbit_gated(v, codes, scales, codes, scales, code_mode=mode(grid), **kw)
+    want, want2 = call(x), call(x2)
     torch.cuda.synchronize()
     s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
-    outs = [(q.lowbit_gated(x, codes, scales, codes, scales, stream=s1),
-             q.lowbit_gated(x2, codes, scales, codes, scales, stream=s2)) for _ in range(8)]
+    outs = [(call(x, stream=s1), call(x2, stream=s2)) for _ in range(8)]
     torch.cuda.synchronize()
     for a, b in outs:
         assert torch.equal(a, want) and torch.equal(b, want2)
-    static = x.clone()
-    g = torch.cuda.CUDAGraph()
-    with torch.cuda.graph(g):
-        out = q.lowbit_gated(static, codes, scales, codes, scales)
-    static.copy_(x2)
-    g.replay()
-    torch.cuda.synchronize()
-    assert torch.equal(out, want2)
+    # back to back on one stream, each input written right before its call and the output read right after
+    static, acc = x.clone(), torch.zeros_like(want, dtype=torch.float64)
+    for i in range(20):
+        static.copy_(x if i % 2 else x2)
+        acc += call(static).double()
+    assert torch.equal(acc, 10 * (want.double() + want2.double()))
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = call(static)
+        graphs.append((g, out))
+    for v, ref_out in ((x2, want2), (x, want)):
+        static.copy_(v)
+        for g, _ in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for _, out in graphs:
+            assert torch.equal(out, ref_out)
+
+
+def test_weights_written_right_before_the_call(cuda_device):
+    # the layer's kernel may start while the one that transforms x runs: codes and scales written by earlier work on the
+    # stream must be seen all the same
+    M, N, K = 16, 2056, 4096
+    codes, scales, w = weight(N, K, "int4", False, seed=17)
+    x = activations(M, K, seed=18)
+    want = q.lowbit_linear(x, codes, scales)
+    cw, sw = torch.empty_like(codes), torch.empty_like(scales)
+    for _ in range(20):
+        cw.zero_()
+        sw.fill_(float("nan"))
+        cw.copy_(codes)
+        sw.copy_(scales)
+        assert torch.equal(q.lowbit_linear(x, cw, sw), want)
+    W = (torch.randn(N, K, device="cuda", generator=gen(19)) * 0.02).to(BF)
+    first = None
+    for _ in range(5):                               # the quantizer's own launch right before
+        qw = q.quantize_fwd(W, 4, mask_mode=None)
+        got = q.lowbit_linear(x, qw["codes"], qw["scales"])
+        first = got if first is None else first
+        assert torch.equal(got, first)
+
+
+@pytest.mark.parametrize("M,N,K,had", [(16, 40, 32768, 128), (9, 24, 32512, 256), (64, 16, 16384, 64)])
+def test_gated_longest_rows(cuda_device, M, N, K, had):
+    cg, sg, wg = weight(N, K, "int4", False, seed=20)
+    cu, su, wu = weight(N, K, "int4", True, seed=21)
+    x = activations(M, K, seed=22)
+    for grid in ("int4", "fp4"):
+        vg = wg if grid == "int4" else ref.scaled(ref.e2m1(cg, N), sg)
+        got = q.lowbit_gated(x, cg, sg, cg, sg, code_mode=mode(grid), had_block=had)
+        a, ea = product(x, vg, had, grid)
+        v, _ = ref.gate(a, "silu")
+        want = v * a
+        tol = (2 ** -8 + 2 ** -16) * want.abs() + 1.13 * ea * (a.abs() + ea) + v.abs() * ea + 1e-38
+        assert ((got.double() - want).abs() <= tol).all()
+    with pytest.raises(q.QuestError, match="one form"):
+        q.lowbit_gated(x, cg, sg, cu, su, had_block=had)
