@@ -85,16 +85,16 @@ def test_decoding_step(cuda_device, code_mode):
     g = gen(3)
     X = torch.randn(40, K, device="cuda", generator=g).to(BF)
     W = [(torch.randn(F, K, device="cuda", generator=g) * K ** -0.5).to(BF) for _ in range(2)]
-    Wd = (torch.randn(K, F, device="cuda", generator=g) * F ** -0.5).to(BF)[:, :1280].contiguous()
+    Wd = (torch.randn(K, F, device="cuda", generator=g) * F ** -0.5).to(BF)[:, :1024].contiguous()
     qg, qu = [q.quantize_fwd(w, 4, code_mode=code_mode, mask_mode=None, dequant="fp32") for w in W]
-    qd = q.quantize_fwd(Wd, 4, rms_group=1280, code_mode=code_mode, mask_mode=None, dequant="fp32")
+    qd = q.quantize_fwd(Wd, 4, rms_group=1024, code_mode=code_mode, mask_mode=None, dequant="fp32")
     x = X[-1:]
     h = q.lowbit_gated(x, qg["codes"], qg["scales"], qu["codes"], qu["scales"], code_mode=code_mode)
-    y = q.lowbit_linear(h[:, :1280], qd["codes"], qd["scales"], code_mode=code_mode)
+    y = q.lowbit_linear(h[:, :1024], qd["codes"], qd["scales"], code_mode=code_mode)
     xt = ref.transform(x.double(), 128)
     want = ref.gate(xt @ qg["dequant"].double().t(), "silu")[0] * (xt @ qu["dequant"].double().t())
     assert (h.double() - want).norm() <= 2 ** -8 * want.norm()
-    want_y = ref.transform(h[:, :1280].double(), 128) @ qd["dequant"].double().t()
+    want_y = ref.transform(h[:, :1024].double(), 128) @ qd["dequant"].double().t()
     assert (y.double() - want_y).norm() <= 2 ** -8 * want_y.norm()
     # prefill: the input in bf16 in the Hadamard domain (rounded to 2^-9 rms of each value), the weights in bf16
     xh = ref.transform(X.double(), 128).to(BF)
