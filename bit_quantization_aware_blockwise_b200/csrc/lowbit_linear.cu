@@ -180,9 +180,8 @@ __device__ __forceinline__ void stage_x(const LowbitParams& p, int m0, int token
             top = max(top, max(__float_as_uint(v[j].x) & 0x7FFFFFFFu, __float_as_uint(v[j].y) & 0x7FFFFFFFu));
 #pragma unroll
         for (int h = 1; h < 8; h <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, h));
-        // word w of token m lies (g tokens + m) 256 + (w ^ (m & 3)) 64 bytes in: eight lanes' 16-byte reads (two
-        // tokens) then touch all 32 banks
-        uint8_t* at = frags + (size_t(g) * tokens + m) * 256 + (u >> 1) * 16;
+        // word w of token m lies ((4 g + w) tokens + m) 64 bytes in: a fragment read is one run of bytes
+        uint8_t* at = frags + (size_t(g) * 4 * tokens + m) * 64 + (u >> 1) * 16;
         const int w0 = 2 * (u & 1);
         float2 entry;
         uint4 out[2];
@@ -230,12 +229,12 @@ __device__ __forceinline__ void stage_x(const LowbitParams& p, int m0, int token
         }
         if (!live) continue;
 #pragma unroll
-        for (int w = 0; w < 2; ++w) *reinterpret_cast<uint4*>(at + (((w0 + w) ^ (m & 3)) << 6)) = out[w];
+        for (int w = 0; w < 2; ++w) *reinterpret_cast<uint4*>(at + (w0 + w) * tokens * 64) = out[w];
         if (u == 0) meta[g * TOK + m] = entry;
     }
 }
 
-// The staged copy of x for token tile `tile`: fragments [groups][tokens][256], and meta [groups][TOK] behind all of them.
+// The staged copy of x for token tile `tile`: fragments [groups][4 words][tokens][64], and meta [groups][TOK] behind all of them.
 template <int TOK>
 __device__ __forceinline__ uint8_t* staged_frags(const LowbitParams& p, int tile) {
     return p.staged + size_t(tile) * TOK * p.groups * 256;
@@ -274,8 +273,6 @@ __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ uint32_t word_of(const uint4& q, int i) { return i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w; }
-
 // NT: tokens / 8.
 template <bool FP4, int NT, bool GATED, int ACT>
 __global__ void __launch_bounds__(kWarps * 32, 1) lowbit_kernel(const LowbitParams p) {
@@ -292,7 +289,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) lowbit_kernel(const LowbitPara
     const int tokens = min(TOK, p.M - m0);
     const int g0 = int(rank) * p.slice, ng = max(min(p.slice, p.groups - g0), 0);
     const int wr = kWarps / p.wk, wrow = warp / p.wk, wkk = warp % p.wk;
-    // shared memory: B fragments [slice][tokens][256], meta [slice][TOK], the warps' scales [kWarps][2][MATS][16 rows]
+    // shared memory: B fragments [slice][4 words][tokens][64], meta [slice][TOK], the warps' scales [kWarps][2][MATS][16 rows]
     // [kChunk], the warps' sums [kWarps][tile] (if they are to be added), and with a cluster this CTA's sums
     // [iters * wr][tile]
     uint8_t* frags = lsmem;
@@ -423,59 +420,78 @@ __global__ void __launch_bounds__(kWarps * 32, 1) lowbit_kernel(const LowbitPara
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int bm = min(nt * 8 + lg, tokens - 1);
-        frag0[nt] = uint32_t(2 * wkk * tokens + bm) * 256 + ((bm & 3) << 6) + lt * 16;   // (from `frags`)
+        frag0[nt] = uint32_t(2 * wkk * 4 * tokens + bm) * 64 + lt * 16;   // (from `frags`)
     }
     const uint32_t meta0 = uint32_t(p.slice) * tokens * 256 + uint32_t(2 * wkk * TOK + 2 * lt) * 8;
     float total[MATS][2][NT][4] = {};        // [matrix][group of the pair]
     int c_buf = 0;                           // the scales' buffer in use
 
-    // one group: rows' codes u0 (lg's) and u1 (lg + 8's), their scales s0 and s1
-    auto group = [&](const uint32_t (&u0)[4], const uint32_t (&u1)[4], float s0, float s1, uint32_t fa, uint32_t ma,
-                     float (&tot)[NT][4]) {
+    // one group of each matrix: rows' codes u[matrix][lg, lg + 8], their scales s
+    auto group = [&](const uint32_t (&u)[MATS][2][4], const float (&s)[MATS][2], uint32_t fa, uint32_t ma, int half) {
         if constexpr (FP4) {
-            float acc[NT][4] = {};
+            float acc[MATS][NT][4] = {};
 #pragma unroll
             for (int w4 = 0; w4 < 4; ++w4) {
-                uint32_t pa[4], pb[4];
-                decode_e2m1(u0[w4], pa);
-                decode_e2m1(u1[w4], pb);
+                uint4 b[NT];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const uint4 b = *reinterpret_cast<const uint4*>(lsmem + ((frag0[nt] ^ (w4 << 6)) + fa));
-                    mma_16816(acc[nt], pa[0], pb[0], pa[1], pb[1], b.x, b.y);
-                    mma_16816(acc[nt], pa[2], pb[2], pa[3], pb[3], b.z, b.w);
+                for (int nt = 0; nt < NT; ++nt)
+                    b[nt] = *reinterpret_cast<const uint4*>(lsmem + (frag0[nt] + fa + w4 * tokens * 64));
+#pragma unroll
+                for (int w = 0; w < MATS; ++w) {
+                    uint32_t pa[4], pb[4];
+                    decode_e2m1(u[w][0][w4], pa);
+                    decode_e2m1(u[w][1][w4], pb);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_16816(acc[w][nt], pa[0], pb[0], pa[1], pb[1], b[nt].x, b[nt].y);
+                        mma_16816(acc[w][nt], pa[2], pb[2], pa[3], pb[3], b[nt].z, b[nt].w);
+                    }
                 }
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const uint4 mm = *reinterpret_cast<const uint4*>(lsmem + (ma + nt * 64));   // two tokens' (0, scale)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    tot[nt][e] = fmaf((e < 2 ? s0 : s1) * __uint_as_float(e & 1 ? mm.w : mm.y), acc[nt][e], tot[nt][e]);
+                for (int w = 0; w < MATS; ++w)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float& t = total[w][half][nt][e];
+                        t = fmaf(s[w][e >> 1] * __uint_as_float(e & 1 ? mm.w : mm.y), acc[w][nt][e], t);
+                    }
             }
         } else {
-            int hi[NT][4] = {}, lo[NT][4] = {};
+            int hi[MATS][NT][4] = {}, lo[MATS][NT][4] = {};
 #pragma unroll
             for (int w4 = 0; w4 < 4; ++w4) {
-                const uint32_t a0 = (u0[w4] & 0x0F0F0F0Fu) ^ 0x08080808u, a1 = (u1[w4] & 0x0F0F0F0Fu) ^ 0x08080808u;
-                const uint32_t a2 = ((u0[w4] >> 4) & 0x0F0F0F0Fu) ^ 0x08080808u;
-                const uint32_t a3 = ((u1[w4] >> 4) & 0x0F0F0F0Fu) ^ 0x08080808u;
+                uint4 b[NT];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const uint4 b = *reinterpret_cast<const uint4*>(lsmem + ((frag0[nt] ^ (w4 << 6)) + fa));
-                    mma_u8s8(hi[nt], a0, a1, a2, a3, b.x, b.y);
-                    mma_u8u8(lo[nt], a0, a1, a2, a3, b.z, b.w);
+                for (int nt = 0; nt < NT; ++nt)
+                    b[nt] = *reinterpret_cast<const uint4*>(lsmem + (frag0[nt] + fa + w4 * tokens * 64));
+#pragma unroll
+                for (int w = 0; w < MATS; ++w) {
+                    const uint32_t u0 = u[w][0][w4], u1 = u[w][1][w4];
+                    const uint32_t a0 = (u0 & 0x0F0F0F0Fu) ^ 0x08080808u, a1 = (u1 & 0x0F0F0F0Fu) ^ 0x08080808u;
+                    const uint32_t a2 = ((u0 >> 4) & 0x0F0F0F0Fu) ^ 0x08080808u;
+                    const uint32_t a3 = ((u1 >> 4) & 0x0F0F0F0Fu) ^ 0x08080808u;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_u8s8(hi[w][nt], a0, a1, a2, a3, b[nt].x, b[nt].y);
+                        mma_u8u8(lo[w][nt], a0, a1, a2, a3, b[nt].z, b[nt].w);
+                    }
                 }
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const uint4 mm = *reinterpret_cast<const uint4*>(lsmem + (ma + nt * 64));   // two tokens' (15 sum(x), half the step)
+                const uint4 mm = *reinterpret_cast<const uint4*>(lsmem + (ma + nt * 64));   // (15 sum(x), half the step)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    // 2 (256 hi + lo) - 15 sum(x), below 2^28 in magnitude
-                    const int v = int(uint32_t(512 * hi[nt][e] + 2 * lo[nt][e]) - (e & 1 ? mm.z : mm.x));
-                    tot[nt][e] = fmaf((e < 2 ? s0 : s1) * __uint_as_float(e & 1 ? mm.w : mm.y), __int2float_rn(v), tot[nt][e]);
-                }
+                for (int w = 0; w < MATS; ++w)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        // 2 (256 hi + lo) - 15 sum(x), below 2^28 in magnitude
+                        const int v = int(uint32_t(512 * hi[w][nt][e] + 2 * lo[w][nt][e]) - (e & 1 ? mm.z : mm.x));
+                        float& t = total[w][half][nt][e];
+                        t = fmaf(s[w][e >> 1] * __uint_as_float(e & 1 ? mm.w : mm.y), __int2float_rn(v), t);
+                    }
             }
         }
     };
@@ -497,25 +513,30 @@ __global__ void __launch_bounds__(kWarps * 32, 1) lowbit_kernel(const LowbitPara
             }
 #pragma unroll
             for (int d = 0; d < kPairs; ++d) {
+                if (live && pair + d < pairs) {
 #pragma unroll
-                for (int w = 0; w < MATS; ++w) {
-                    uint4 (&qd)[4] = q[d][w];
-                    if (live && pair + d < pairs) {
+                    for (int h = 0; h < 2; ++h) {
+                        if (h == 1 && ragged && pair + d + 1 == pairs) break;
+                        // even lanes: rows lg from loads 0 and 2 in the first group, lg + 1 from 1 and 3 in the
+                        // second; odd lanes the other way round
+                        uint32_t u[MATS][2][4];
+                        float sv[MATS][2];
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            // even lanes: rows lg from loads 0 and 2 in the first group, lg + 1 from 1 and 3 in the
-                            // second; odd lanes the other way round
-                            const uint4 a = odd == (h != 0) ? qd[0] : qd[1], b = odd == (h != 0) ? qd[2] : qd[3];
-                            const uint32_t u0[4] = {a.x, a.y, a.z, a.w}, u1[4] = {b.x, b.y, b.z, b.w};
+                        for (int w = 0; w < MATS; ++w) {
+                            const uint4 a = odd == (h != 0) ? q[d][w][0] : q[d][w][1];
+                            const uint4 b = odd == (h != 0) ? q[d][w][2] : q[d][w][3];
+                            u[w][0][0] = a.x; u[w][0][1] = a.y; u[w][0][2] = a.z; u[w][0][3] = a.w;
+                            u[w][1][0] = b.x; u[w][1][1] = b.y; u[w][1][2] = b.z; u[w][1][3] = b.w;
                             const float* s = c_scale + (w * 16 + (lg ^ h)) * kChunk +
                                              (by_row ? 0 : (2 * (pair + d) + h) % kChunk);
-                            if (h == 0 || !(ragged && pair + d + 1 == pairs))
-                                group(u0, u1, s[0], s[8 * kChunk], frag_at + h * tokens * 256, meta_at + h * TOK * 8,
-                                      total[w][h]);
+                            sv[w][0] = s[0];
+                            sv[w][1] = s[8 * kChunk];
                         }
+                        group(u, sv, frag_at + h * tokens * 256, meta_at + h * TOK * 8, h);
                     }
-                    load(qd, w, d == kPairs - 1);
                 }
+#pragma unroll
+                for (int w = 0; w < MATS; ++w) load(q[d][w], w, d == kPairs - 1);
                 frag_at += p.wk * tokens * 512;
                 meta_at += p.wk * TOK * 16;
             }
