@@ -72,6 +72,7 @@ struct LowbitParams {
     int slice;           // groups per CTA of the cluster (even, but for a single CTA's last)
     int wk;              // warps along K
     int iters;           // row tiles per warp
+    int batch;           // of them, those whose sums a cluster collects at a time
     int clusters;
     float had_scale;     // 1 / sqrt(had)
 };
@@ -291,7 +292,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) lowbit_kernel(const LowbitPara
     const int wr = kWarps / p.wk, wrow = warp / p.wk, wkk = warp % p.wk;
     // shared memory: B fragments [slice][4 words][tokens][64], meta [slice][TOK], the warps' scales [kWarps][2][MATS][16 rows]
     // [kChunk], the warps' sums [kWarps][tile] (if they are to be added), and with a cluster this CTA's sums
-    // [iters * wr][tile]
+    // [batch * wr][tile]
     uint8_t* frags = lsmem;
     float2* meta = reinterpret_cast<float2*>(lsmem + size_t(p.slice) * tokens * 256);
     float* scales = reinterpret_cast<float*>(meta + p.slice * TOK) + warp * (2 * MATS * 16 * kChunk);
@@ -425,6 +426,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) lowbit_kernel(const LowbitPara
     const uint32_t meta0 = uint32_t(p.slice) * tokens * 256 + uint32_t(2 * wkk * TOK + 2 * lt) * 8;
     float total[MATS][2][NT][4] = {};        // [matrix][group of the pair]
     int c_buf = 0;                           // the scales' buffer in use
+    int held = 0;                            // tile steps whose sums wait for the cluster
+    const uint32_t hold_addr = static_cast<uint32_t>(__cvta_generic_to_shared(hold));
 
     // one group of each matrix: rows' codes u[matrix][lg, lg + 8], their scales s
     auto group = [&](const uint32_t (&u)[MATS][2][4], const float (&s)[MATS][2], uint32_t fa, uint32_t ma, int half) {
@@ -542,7 +545,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) lowbit_kernel(const LowbitPara
             }
         }
         // the tile's sums
-        float* dst = (direct ? hold + (it * wr + wrow) * kTile : part + warp * kTile) + lg;
+        float* dst = (direct ? hold + (held * wr + wrow) * kTile : part + warp * kTile) + lg;
 #pragma unroll
         for (int w = 0; w < MATS; ++w)
 #pragma unroll
@@ -554,7 +557,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) lowbit_kernel(const LowbitPara
                     dst[(w * TOK + nt * 8 + 2 * lt + (e & 1)) * 16 + 8 * (e >> 1)] = t;
                     total[w][0][nt][e] = total[w][1][nt][e] = 0.0f;
                 }
-        if (direct) continue;
         // the tile's wk warps: all sums written, and below all read before the next tile's
         auto meet = [&]() {
             if (p.wk > 1)
@@ -562,54 +564,57 @@ __global__ void __launch_bounds__(kWarps * 32, 1) lowbit_kernel(const LowbitPara
             else
                 __syncwarp();
         };
-        meet();
-        const float* src = part + wrow * p.wk * kTile;
-        for (int i = wkk * 32 + lane; i < 16 * tokens; i += 32 * p.wk) {
-            float v[MATS] = {};
-            for (int k = 0; k < p.wk; ++k)
+        if (!direct) {
+            meet();
+            const float* src = part + wrow * p.wk * kTile;
+            for (int i = wkk * 32 + lane; i < 16 * tokens; i += 32 * p.wk) {
+                float v[MATS] = {};
+                for (int k = 0; k < p.wk; ++k)
 #pragma unroll
-                for (int w = 0; w < MATS; ++w) v[w] += src[k * kTile + w * TOK * 16 + i];
-            if (cs > 1) {
+                    for (int w = 0; w < MATS; ++w) v[w] += src[k * kTile + w * TOK * 16 + i];
+                if (cs > 1) {
 #pragma unroll
-                for (int w = 0; w < MATS; ++w) hold[(it * wr + wrow) * kTile + w * TOK * 16 + i] = v[w];
-            } else if (row0 + (i & 15) < p.N) {
+                    for (int w = 0; w < MATS; ++w) hold[(held * wr + wrow) * kTile + w * TOK * 16 + i] = v[w];
+                } else if (row0 + (i & 15) < p.N) {
+                    float out = v[0];
+                    if constexpr (GATED) out = v[0] * gate_sigmoid<ACT>(v[0]) * v[1];
+                    p.y[int64_t(m0 + (i >> 4)) * p.N + row0 + (i & 15)] = __float2bfloat16_rn(out);
+                }
+            }
+            meet();
+        }
+        // in a cluster: a batch of tiles at a time, summed in rank order; the CTAs share the outputs
+        if (cs > 1 && (++held == p.batch || it + 1 == p.iters)) {
+            cluster_barrier();
+            const int first = it + 1 - held, outs = held * wr * 16 * tokens;
+            for (int i = int(rank) * kWarps * 32 + threadIdx.x; i < outs; i += int(cs) * kWarps * 32) {
+                const int slot = i / (16 * tokens), at = i - slot * (16 * tokens);
+                const int64_t row =
+                    ((int64_t(first + slot / wr) * p.clusters + cluster) * wr + slot % wr) * 16 + (at & 15);
+                if (row >= p.N) continue;
+                float v[MATS] = {};
+                for (uint32_t c = 0; c < cs; ++c) {
+                    uint32_t base;
+                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(base) : "r"(hold_addr), "r"(c));
+#pragma unroll
+                    for (int w = 0; w < MATS; ++w) {
+                        float f;
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                                     : "=f"(f)
+                                     : "r"(base + uint32_t(slot * kTile + w * TOK * 16 + at) * 4)
+                                     : "memory");
+                        v[w] += f;
+                    }
+                }
                 float out = v[0];
                 if constexpr (GATED) out = v[0] * gate_sigmoid<ACT>(v[0]) * v[1];
-                p.y[int64_t(m0 + (i >> 4)) * p.N + row0 + (i & 15)] = __float2bfloat16_rn(out);
+                p.y[int64_t(m0 + (at >> 4)) * p.N + row] = __float2bfloat16_rn(out);
             }
+            // no sum is overwritten, and no CTA leaves, while another may still read them
+            cluster_barrier();
+            held = 0;
         }
-        meet();
     }
-    if (cs == 1) return;
-
-    // ---- sum over the cluster, in rank order
-    cluster_barrier();
-    const uint32_t hold_addr = static_cast<uint32_t>(__cvta_generic_to_shared(hold));
-    const int outs = p.iters * wr * 16 * tokens;
-    for (int i = int(rank) * kWarps * 32 + threadIdx.x; i < outs; i += int(cs) * kWarps * 32) {
-        const int slot = i / (16 * tokens), at = i - slot * (16 * tokens);
-        const int64_t row = ((int64_t(slot / wr) * p.clusters + cluster) * wr + slot % wr) * 16 + (at & 15);
-        if (row >= p.N) continue;
-        float v[MATS] = {};
-        for (uint32_t c = 0; c < cs; ++c) {
-            uint32_t base;
-            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(base) : "r"(hold_addr), "r"(c));
-#pragma unroll
-            for (int w = 0; w < MATS; ++w) {
-                float f;
-                asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                             : "=f"(f)
-                             : "r"(base + uint32_t(slot * kTile + w * TOK * 16 + at) * 4)
-                             : "memory");
-                v[w] += f;
-            }
-        }
-        float out = v[0];
-        if constexpr (GATED) out = v[0] * gate_sigmoid<ACT>(v[0]) * v[1];
-        p.y[int64_t(m0 + (at >> 4)) * p.N + row] = __float2bfloat16_rn(out);
-    }
-    // no CTA leaves while another may still read its sums
-    cluster_barrier();
 }
 
 // Clusters of a kernel that run at the same time on the current device, by cluster size and shared memory.
@@ -673,8 +678,8 @@ cudaError_t launch_one(const LowbitArgs& a, cudaStream_t stream) {
     cfg.stream = stream;
 
     // CTAs along K (cs) and warps along K (wk): the pair with the least work for the busiest warp, counted in
-    // groups: its row tiles, each ceil(slice / wk) groups and a sum over the warps worth about three (one more
-    // over the cluster). Larger clusters leave SMs empty (their CTAs share a GPC), so the clusters that run at once are asked
+    // groups: its row tiles, each ceil(slice / wk) groups and a sum over the warps worth about three, and
+    // each batch's sum over the cluster about four. Larger clusters leave SMs empty (their CTAs share a GPC), so the clusters that run at once are asked
     // of the runtime. Shared memory must hold the slice of x, the warps' sums and, in a cluster, every tile's sums.
     constexpr size_t kRoom = 226 * 1024;
     static_assert(kLowbitMaxK / kGroup / kMaxCluster * (TOK * 256 + TOK * 8) + kWarps * (2 * MATS * 16 * kChunk * 4) +
@@ -696,18 +701,19 @@ cudaError_t launch_one(const LowbitArgs& a, cudaStream_t stream) {
         for (int wk = 1; wk <= kWarps && (wk == 1 || 2 * wk <= slice + 1); wk *= 2) {
             const int side = kWarps / wk;
             const int64_t turns = (tiles + side - 1) / side;
-            int64_t iters = (turns + wave - 1) / wave;
+            const int64_t iters = (turns + wave - 1) / wave;
             size_t need = fixed + (c > 1 && wk == 1 ? 0 : kWarps * kTileBytes);
             if (need > kRoom) continue;
-            if (c > 1) {   // (a long walk over the tiles is cut where their sums fill shared memory)
-                const int64_t most = int64_t((kRoom - need) / (side * kTileBytes));
-                if (most < 1) continue;
-                if (iters > most) iters = most;
-                need += size_t(iters) * side * kTileBytes;
+            int64_t batch = iters;
+            if (c > 1) {   // as many tiles at a time as shared memory holds sums of
+                batch = int64_t((kRoom - need) / (side * kTileBytes));
+                if (batch < 1) continue;
+                if (batch > iters) batch = iters;
+                need += size_t(batch) * side * kTileBytes;
             }
-            const int64_t used = (turns + iters - 1) / iters, waves = (used + wave - 1) / wave;
+            const int64_t used = (turns + iters - 1) / iters;
             const int per_warp = ((slice + 1) / 2 + wk - 1) / wk;
-            const int64_t cost = waves * iters * (2 * per_warp + 3 + (c > 1));
+            const int64_t cost = iters * (2 * per_warp + 3) + (c > 1 ? (iters + batch - 1) / batch * 4 : 0);
             if (cs == 0 || cost < best) {
                 best = cost;
                 cs = c;
@@ -716,6 +722,7 @@ cudaError_t launch_one(const LowbitArgs& a, cudaStream_t stream) {
                 p.wk = wk;
                 p.slice = slice;
                 p.iters = (int)iters;
+                p.batch = (int)batch;
             }
         }
     }

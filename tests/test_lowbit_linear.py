@@ -69,7 +69,7 @@ def test_matches_formula(cuda_device, M, N, K, had, rows, grid):
 
 @pytest.mark.parametrize("grid", ["int4", "fp4"])
 @pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
-@pytest.mark.parametrize("M,F,K,had", [(1, 8, 128, 128), (1, 5632, 2048, 128), (3, 136, 256, 256), (16, 520, 640, 0),
+@pytest.mark.parametrize("M,F,K,had", [(1, 8, 128, 128), (1, 5632, 2048, 128), (3, 136, 256, 256), (16, 520, 640, 0), (16, 22016, 8192, 128), (40, 11008, 4096, 256),
                                        (33, 264, 512, 64)])
 def test_gated_matches_formula(cuda_device, M, F, K, had, act, grid):
     cg, sg, wg = weight(F, K, grid, False, seed=1)
