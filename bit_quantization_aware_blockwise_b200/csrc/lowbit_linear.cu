@@ -279,7 +279,11 @@ template <bool FP4, int NT, bool GATED, int ACT>
 __global__ void __launch_bounds__(kWarps * 32, 1) lowbit_kernel(const LowbitParams p) {
     extern __shared__ __align__(256) uint8_t lsmem[];
     constexpr int MATS = GATED ? 2 : 1, TOK = 8 * NT;
-    constexpr int kPairs = GATED ? 1 : 2;    // pairs of groups in registers (of each matrix), and per turn of the loop
+    // Pairs of groups in registers (of each matrix), and per turn of the loop, as registers allow. One matrix, up to 8
+    // tokens: 44032 x 8192 took 59, 54 and 51 us with 1, 2 and 4; 16 tokens x 8192 x 22016: 41, 40 and 56. Two matrices:
+    // 22016 x 8192 took 52 us with one of each, 61 with two.
+    constexpr int kPairs = GATED ? 1 : NT == 1 ? 4 : 2;
+    static_assert(kChunk % (2 * kPairs) == 0, "a turn lies in one chunk of scales");
     constexpr int kTile = MATS * TOK * 16;   // one tile's sums, [matrix][token][row]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t rank, cs;
