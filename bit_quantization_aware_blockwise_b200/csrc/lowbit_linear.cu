@@ -757,6 +757,8 @@ cudaError_t launch_grid(const LowbitArgs& a, cudaStream_t stream) {
 }  // namespace
 
 // x is transformed by a kernel of its own from this many (token, group) items on; below, every CTA transforms its slice.
+// With the limit at 64, 128, 256 and 512: 8 x 5632 x 2048 8.3, 8.2, 10.3 and 10.3 us, 4 x 2048 x 8192 8.9, 8.2, 8.2
+// and 12.3, 16 x 2048 x 2048 8.2, 8.2, 8.2 and 12.1 (replayed graphs).
 constexpr int64_t kStageItems = 128;
 
 size_t lowbit_workspace_bytes(int64_t M, int64_t K) {

@@ -26,8 +26,8 @@ namespace {
 // onto 2^15, minus the offset, times the token's step, rounded to bf16, as the quantizer's dequant is but for
 // rare ties): 3 bytes moved per value. The product then runs at the tensor cores' rate. Restoring inside
 // the product's mainloop instead repeats the work for every 256 rows of G: eight conversion warps
-// beside the MMAs took 694 us at 16384 x 11264 x 2048, of which 190 us went away with the
-// conversion's arithmetic and stores taken out; the pass costs about 20.
+// beside the MMAs took 694 us at 16384 x 11264 x 2048 (541 with the conversion's arithmetic and stores
+// taken out) where the pass costs 20 us and all of it 502.
 //
 // The reduction runs over the tokens, the outer dimension of both operands, so the MMA
 // takes both transposed (MN-major): a stage row is one token's 64 columns (128 bytes,
@@ -541,8 +541,9 @@ __global__ void __launch_bounds__(256) weight_grad_finish_kernel(const float4* _
 }
 
 // Token splits: with fewer output tiles than CTA pairs, the tokens are cut so that the pairs left idle
-// take part, in pieces of at least kMinBlocks blocks of 64 tokens (a piece costs its partial's
-// round trip through the workspace, 256 KB a tile, worth about that many blocks of MMAs).
+// take part, in pieces of at least kMinBlocks blocks of 64 tokens (a piece costs its partial's round trip
+// through the workspace, 256 KB a tile, and the finishing launch). 8192 x 512 x 512 takes 22.5 us so and 47 uncut,
+// 3001 x 520 x 384 15.6 and 23; with pieces of at least 2, 4 and 16 blocks the latter takes 16.4, 16.4 and 18.5.
 constexpr int kMinBlocks = 8;
 
 struct SplitPlan {
