@@ -157,7 +157,9 @@ __device__ __forceinline__ void stage_x(const LowbitParams& p, int m0, int token
             const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                v[4 * c + j] = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
+                // (taken down by 2^8, exactly, so that no sum of 256 finite values overflows; the group's scale makes it up)
+                v[4 * c + j] = __fmul2_rn(make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u)),
+                                          make_float2(0.00390625f, 0.00390625f));
         }
         fetch_x(p, m0, items, g0, ng, base + warps * 4, raw);
         if (p.had) {
@@ -187,9 +189,9 @@ __device__ __forceinline__ void stage_x(const LowbitParams& p, int m0, int token
         float2 entry;
         uint4 out[2];
         if constexpr (FP4) {
-            const uint32_t e = max(top >> 23, 20u);   // (values below 2^-107 fade into zeros)
+            const uint32_t e = max(top >> 23, 20u);   // (groups below 2^-99 fade into zeros)
             const float mul = __uint_as_float((268u - e) << 23);
-            entry = make_float2(0.0f, __uint_as_float((e - 14u) << 23) * p.had_scale);
+            entry = make_float2(0.0f, __uint_as_float((e - 14u) << 23) * (256.0f * p.had_scale));
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
                 uint32_t h[4];
@@ -203,8 +205,8 @@ __device__ __forceinline__ void stage_x(const LowbitParams& p, int m0, int token
         } else {
             // the group's largest value becomes 32767; a group below 2^-100 counts as zero
             const float amax = __uint_as_float(top);
-            const bool zero = amax < 7.888609052210118e-31f;
-            const float mul = zero ? 0.0f : __fdividef(32767.0f, amax);
+            const bool zero = amax < 3.0814879110195774e-33f;   // (2^-108, after the 2^-8)
+            const float mul = zero ? 0.0f : 32767.0f / amax;
             uint32_t sum = 0;   // (two's complement; a non-finite group's wraps)
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
@@ -226,7 +228,7 @@ __device__ __forceinline__ void stage_x(const LowbitParams& p, int m0, int token
 #pragma unroll
             for (int h = 1; h < 8; h <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, h);
             // 15 sum(x), and half the step of x (a non-finite largest value makes it non-finite)
-            entry = make_float2(__uint_as_float(15u * sum), zero ? 0.0f : amax * p.had_scale * (0.5f / 32767.0f));
+            entry = make_float2(__uint_as_float(15u * sum), zero ? 0.0f : amax * (p.had_scale * (128.0f / 32767.0f)));
         }
         if (!live) continue;
 #pragma unroll

@@ -102,6 +102,18 @@ def test_quantizer_codes_decode(cuda_device):
             check_linear(got, x, qw["dequant"].double(), 128, grid)
 
 
+@pytest.mark.parametrize("grid,had", [("int4", 128), ("fp4", 128), ("int4", 256), ("fp4", 0)])
+def test_largest_inputs_do_not_overflow(cuda_device, grid, had):
+    # values up to the end of bf16's range, whose plain sums over a block pass fp32's; the results stay inside it
+    codes, scales, w = weight(40, 512, grid, False, seed=23)
+    x = activations(3, 512, seed=24).float()
+    x = (x / x.abs().amax() * 3.3e38).to(BF)
+    scales, w = scales * 2.0 ** -8, w * 2.0 ** -8
+    got = q.lowbit_linear(x, codes, scales, code_mode=mode(grid), had_block=had)
+    assert got.isfinite().all()
+    check_linear(got, x, w, had, grid)
+
+
 def test_scale_of_the_input(cuda_device):
     # very small and very large tokens side by side, a zero token, a group of zeros
     N, K = 40, 512
