@@ -5,9 +5,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <map>
 #include <mutex>
-#include <tuple>
 
 #include "gated_act.cuh"
 #include "quest_internal.h"
@@ -623,21 +621,28 @@ __global__ void __launch_bounds__(kWarps * 32, 1) lowbit_kernel(const LowbitPara
     }
 }
 
-// Clusters of a kernel that run at the same time on the current device, by cluster size and shared memory.
+// Clusters of `cs` CTAs of a kernel that run at the same time on the current device (asked once per kernel, device
+// and cs, at the shared memory in cfg).
 int active_clusters(const void* kernel, const cudaLaunchConfig_t& cfg, int cs) {
+    struct Entry {
+        const void* kernel;
+        int dev, cs, n;
+    };
+    constexpr int kSlots = 96;   // more than the kernels times the cluster sizes of one device; older entries give way
+    static Entry cache[kSlots] = {};
+    static int next = 0;
     static std::mutex mu;
-    static std::map<std::tuple<int, const void*, int, size_t>, int> cache;
     int dev = 0, n = 0;
     cudaGetDevice(&dev);
     std::lock_guard<std::mutex> lock(mu);
-    const auto key = std::make_tuple(dev, kernel, cs, cfg.dynamicSmemBytes);
-    auto it = cache.find(key);
-    if (it != cache.end()) return it->second;
+    for (const Entry& e : cache)
+        if (e.kernel == kernel && e.dev == dev && e.cs == cs) return e.n;
     if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
         cudaGetLastError();
         n = sm_count() / cs > 0 ? sm_count() / cs : 1;
     }
-    cache[key] = n;
+    cache[next] = {kernel, dev, cs, n};
+    next = (next + 1) % kSlots;
     return n;
 }
 
