@@ -304,9 +304,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) lowbit_kernel(const LowbitPara
     const bool direct = p.wk == 1 && cs > 1;   // a warp's sums are the CTA's
     float* hold = direct ? part : part + kWarps * kTile;
 
-    // stage_kernel, if there is one, lets this grid start only after it has itself waited for all earlier work, so the
-    // weights may be read while it runs; x's fragments (and y) wait for its end
-    if (!p.staged) pdl_wait();
+    // Earlier writes on the stream, the codes and scales among them, are visible here only behind this grid's own wait,
+    // so nothing is read ahead of it, although stage_kernel reads no weights.
+    pdl_wait();
 
     const int lg = lane >> 2, lt = lane & 3;
     const bool odd = lg & 1;
@@ -408,7 +408,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) lowbit_kernel(const LowbitPara
         for (int w = 0; w < MATS; ++w) load(q[d][w], w, d == kPairs - 1);
     fetch_scales();
     if (p.staged) {
-        pdl_wait();
         const uint8_t* src = staged_frags<TOK>(p, blockIdx.y) + size_t(g0) * tokens * 256;
         for (int i = threadIdx.x; i < ng * tokens * 16; i += kWarps * 32) copy16_async(frags + 16 * i, src + 16 * i);
         const float2* msrc = staged_meta<TOK>(p, blockIdx.y) + size_t(g0) * TOK;
@@ -764,8 +763,8 @@ cudaError_t launch_grid(const LowbitArgs& a, cudaStream_t stream) {
 }  // namespace
 
 // x is transformed by a kernel of its own from this many (token, group) items on; below, every CTA transforms its slice.
-// With the limit at 64, 128, 256 and 512: 8 x 5632 x 2048 8.3, 8.2, 10.3 and 10.3 us, 4 x 2048 x 8192 8.9, 8.2, 8.2
-// and 12.3, 16 x 2048 x 2048 8.2, 8.2, 8.2 and 12.1 (replayed graphs).
+// With the limit at 64, 128, 256 and 512 (replayed graphs of 24 calls): 4 x 5632 x 2048 6.9, 6.5, 6.5 and 6.5 us, 8 x 2048
+// x 2048 6.2, 6.2, 7.1 and 7.1, 16 x 2048 x 2048 6.4, 6.5, 6.5 and 9.5, 4 x 2048 x 8192 7.7, 7.6, 7.7 and 10.6.
 constexpr int64_t kStageItems = 128;
 
 size_t lowbit_workspace_bytes(int64_t M, int64_t K) {

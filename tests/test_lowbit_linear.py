@@ -238,3 +238,44 @@ def test_gated_longest_rows(cuda_device, M, N, K, had):
         assert ((got.double() - want).abs() <= tol).all()
     with pytest.raises(q.QuestError, match="one form"):
         q.lowbit_gated(x, cg, sg, cu, su, had_block=had)
+
+
+@pytest.mark.parametrize("rms", [128, 4096])
+@pytest.mark.parametrize("M,gated", [(1, False), (16, False), (16, True), (40, False)])
+def test_two_weights_in_turn_in_the_same_buffers(cuda_device, M, gated, rms):
+    # the quantizer, which lets its dependents start early, writes one of two different weights into the same codes and
+    # scales right before each call, with nothing in between: stale codes or scales give the other weight's result
+    N, K = 2056, 4096
+    g = gen(25)
+    W = [(torch.randn(N, K, device="cuda", generator=g) * 0.02).to(BF) for _ in range(2)]
+    x = activations(M, K, seed=26)
+    want = []
+    for w in W:
+        qw = q.quantize_fwd(w, 4, rms_group=rms, mask_mode=None, dequant="fp32")
+        y, err = product(x, qw["dequant"].double(), 128, "int4")
+        if gated:
+            v, _ = ref.gate(y, "silu")
+            y, err = v * y, 2 ** -16 * (v * y).abs() + 1.13 * err * (y.abs() + err) + v.abs() * err
+        want.append((y, 2 ** -8 * y.abs() + err))
+    codes = torch.zeros(N * K // 2, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(N, K // rms, device="cuda")
+    outs = [torch.zeros((M, N), dtype=BF, device="cuda") for _ in range(60)]
+    need = q.lowbit_workspace(M, K)
+    assert (need > 0) == (M >= 16)
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+    st = torch.cuda.current_stream().cuda_stream
+    torch.cuda.synchronize()
+    for i, y in enumerate(outs):
+        q.quantize_fwd_raw(W[i % 2].data_ptr(), q.BF16, N, K, K, 4, 128, rms, 1.0, q.CODES_PACKED, codes.data_ptr(),
+                           scales.data_ptr(), q.MASK_BITS, None, None, q.BF16, st)
+        if gated:
+            q.lowbit_gated_raw(x.data_ptr(), K, codes.data_ptr(), scales.data_ptr(), codes.data_ptr(), scales.data_ptr(),
+                               q.CODES_PACKED, rms, M, N, K, 128, q.ACT_SILU, y.data_ptr(), ws.data_ptr(), need, st)
+        else:
+            q.lowbit_linear_raw(x.data_ptr(), K, codes.data_ptr(), q.CODES_PACKED, scales.data_ptr(), rms, M, N, K, 128,
+                                y.data_ptr(), ws.data_ptr(), need, st)
+    q.device_status()
+    for i, y in enumerate(outs):
+        value, tol = want[i % 2]
+        assert ((y.double() - value).abs() <= tol).all()
+        assert torch.equal(y, outs[i % 2])
