@@ -58,6 +58,9 @@ bool valid_act(quest_act a) { return a == QUEST_ACT_SILU || a == QUEST_ACT_GELU_
 
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 
+// Whether a matrix of a x b elements (both >= 0) is one the block's calls take: its bytes, and bits, fit 64 bits by far.
+bool fits(int64_t a, int64_t b) { return a == 0 || b <= (int64_t(1) << 44) / a; }
+
 bool valid_had(int hb) { return hb == 16 || hb == 32 || hb == 64 || hb == 128 || hb == 256; }
 
 // Longest row the one-RMS-per-row kernel keeps in registers: 2 passes of
@@ -828,7 +831,7 @@ quest_status quest_gated_linear(const void* x_hat, const void* w_gate, const voi
     if ((ckpt_codes == nullptr) != (ckpt_scales == nullptr))
         return fail(QUEST_EINVAL, "ckpt_codes and ckpt_scales must be given together");
     if (M > 0 && F > 0) {
-        if (M > (int64_t(1) << 44) / F) return fail(QUEST_EINVAL, "M * F must be <= 2^44");
+        if (!fits(M, F) || !fits(M, K) || !fits(F, K)) return fail(QUEST_EINVAL, "M * F, M * K and F * K must be <= 2^44");
         if (!h) return fail(QUEST_EINVAL, "h must be non-NULL");
         if (K > 0 && (!x_hat || !w_gate || !w_up)) return fail(QUEST_EINVAL, "x_hat, w_gate and w_up must be non-NULL");
         if (!aligned(h, 16) || !aligned(ckpt_codes, 16) ||
@@ -863,6 +866,7 @@ quest_status quest_gated_bwd(const void* grad_h, const int8_t* ckpt_codes, const
     if (F % 16 != 0) return fail(QUEST_EINVAL, "F must be a multiple of 16");
     if (!valid_act(act)) return fail(QUEST_EINVAL, "invalid act");
     if (M > 0 && F > 0) {
+        if (!fits(M, F)) return fail(QUEST_EINVAL, "M * F must be <= 2^44");
         if (!grad_h || !ckpt_codes || !ckpt_scales || !grad_ab)
             return fail(QUEST_EINVAL, "grad_h, ckpt_codes, ckpt_scales and grad_ab must be non-NULL");
         if (!aligned(grad_h, 16) || !aligned(ckpt_codes, 16) || !aligned(grad_ab, 16) || !aligned(h, 16))
@@ -885,6 +889,7 @@ quest_status quest_gated_bwd(const void* grad_h, const int8_t* ckpt_codes, const
 
 size_t quest_weight_grad_workspace(int64_t T, int64_t N, int64_t K) {
     if (T < 0 || N < 0 || K < 0 || T > kMaxDim || N > kMaxDim || K > kMaxDim || N % 8 != 0 || K % 128 != 0) return 0;
+    if (!fits(N, K) || !fits(T, K)) return 0;
     return weight_grad_workspace_bytes(T, N, K);
 }
 
@@ -912,7 +917,7 @@ quest_status quest_weight_grad(const void* grad_y, int64_t ld_gy, const void* co
     if (accumulate && out_dtype != QUEST_FP32) return fail(QUEST_EINVAL, "accumulate needs an fp32 gradient");
     const int cb = code_bits(bits, code_mode);
     if (N > 0 && K > 0) {
-        if (N > (int64_t(1) << 44) / K) return fail(QUEST_EINVAL, "N * K must be <= 2^44");
+        if (!fits(N, K) || !fits(T, K) || !fits(T, ld_gy)) return fail(QUEST_EINVAL, "N * K, T * K and T * ld_gy must be <= 2^44");
         if (!grad_w) return fail(QUEST_EINVAL, "grad_w must be non-NULL");
         if (T > 0 && (!grad_y || !codes || !scales)) return fail(QUEST_EINVAL, "grad_y, codes and scales must be non-NULL");
         if (!aligned(grad_w, 16) || !aligned(mask, 16) || (T > 0 && (!aligned(grad_y, 16) || !aligned(codes, 16))))

@@ -454,7 +454,8 @@ quest_status quest_transpose_bf16(const void* src, int64_t rows, int64_t cols, v
  *
  * Arguments
  *   x_hat    device bf16 [M, K].   w_gate, w_up   device bf16 [F, K].
- *   M, F, K  >= 0; F a multiple of 16, K a multiple of 8; each < 2^31. K == 0 gives h = 0.
+ *   M, F, K  >= 0; F a multiple of 16, K a multiple of 8; M, K < 2^31, F < 2^30, M F, M K and F K at most 2^44.
+ *            K == 0 gives h = 0.
  *   act      the activation.
  *   h        device bf16 [M, F].
  *   ckpt_codes, ckpt_scales   device int8 [M, 2 F] (a's codes, then b's) and fp32
@@ -478,7 +479,7 @@ quest_status quest_gated_linear(const void* x_hat, const void* w_gate, const voi
  *
  * Arguments
  *   grad_h   device bf16 [M, F].   ckpt_codes, ckpt_scales   as quest_gated_linear wrote them.
- *   M, F     >= 0; F a multiple of 16; each < 2^31.   act as in the forward.
+ *   M, F     >= 0; F a multiple of 16; M < 2^31, F < 2^30, M F at most 2^44.   act as in the forward.
  *   grad_ab  device bf16 [M, 2 F]: grad_a in columns 0..F-1, grad_b after them.
  *   h        device bf16 [M, F], or NULL: the block's output again, from the restored a and b.
  * All pointers 16-byte aligned (ckpt_scales 4-byte); outputs overlap nothing.
@@ -510,7 +511,8 @@ quest_status quest_gated_bwd(const void* grad_h, const int8_t* ckpt_codes, const
  *   scales   device fp32 [T, K / rms_group]; rms_group 128 or K.
  *   mask     device, the weight's trust mask bits [N, K / 8] (QUEST_MASK_BITS layout), 16-byte
  *            aligned, or NULL (every entry kept).
- *   T, N, K  >= 0 and < 2^31; N a multiple of 8, K a multiple of 128. T == 0 is the empty sum.
+ *   T, N, K  >= 0 and < 2^31; N a multiple of 8, K a multiple of 128; N K, T K and T ld_gy at most 2^44.
+ *            T == 0 is the empty sum.
  *   had_block  128 (QUEST_EUNSUPPORTED otherwise).
  *   grad_w   device out_dtype [N, K], 16-byte aligned; overlaps nothing.
  *   accumulate   0: grad_w is overwritten. 1: the gradient is added to it, in fp32 (out_dtype

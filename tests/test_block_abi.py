@@ -108,3 +108,29 @@ def test_wrappers_refuse_host_tensors():
                  lambda: q.lowbit_gated(x, codes, scales, codes, scales)):
         with pytest.raises(q.QuestError, match="CUDA tensor"):
             call()
+
+
+BIG = (1 << 31) - 128   # a multiple of 128
+
+
+@pytest.mark.parametrize("call,kw,what", [
+    (weight_grad, dict(T=BIG, N=8, ld=8, K=BIG), "T * K"),
+    (weight_grad, dict(T=1 << 30, N=8, ld=8, K=1 << 15), "T * K"),
+    (weight_grad, dict(T=BIG, N=8, ld=BIG, K=128), "T * ld_gy"),
+    (weight_grad, dict(T=4, N=1 << 30, ld=1 << 30, K=1 << 30), "N * K"),
+    (gated_linear, dict(M=BIG, F=16, K=BIG), "M * K"),
+    (gated_linear, dict(M=1, F=1 << 29, K=BIG), "F * K"),
+    (gated_bwd, dict(M=BIG, F=1 << 29), "M * F"),
+])
+def test_sizes_whose_products_pass_64_bits_are_refused(call, kw, what):
+    # before any byte count is formed from them (and, with the largest workspace a caller can claim, before any launch)
+    if call is weight_grad:
+        kw = dict(kw, ws_bytes=(1 << 64) - 1)
+    assert call(**kw) == EINVAL
+    assert what in q.load_library().quest_last_error_message().decode()
+
+
+def test_workspace_query_of_impossible_sizes():
+    assert q.weight_grad_workspace(BIG, 8, BIG) == 0
+    assert q.weight_grad_workspace(8, BIG, BIG) == 0
+    assert q.weight_grad_workspace(1 << 29, 8, 1 << 14) >= 1 << 44
