@@ -276,7 +276,9 @@ def _torch():
 def _stream_handle(stream, device):
     if stream is not None:
         return stream.cuda_stream
-    return _torch()._C._cuda_getCurrentRawStream(device.index)   # torch.cuda.current_stream(device).cuda_stream, 2 us sooner
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # the public call's answer, 2 us sooner
+    return raw(device.index) if raw is not None else torch.cuda.current_stream(device).cuda_stream
 
 
 def _require_cuda(t, name):
@@ -592,8 +594,10 @@ _HERE_ALREADY = contextlib.nullcontext()
 
 def _at(device, stream):
     """The context of a call on ``device``: none where it is the current one and no stream is given."""
-    if stream is None and _torch()._C._cuda_getDevice() == device.index:
-        return _HERE_ALREADY
+    if stream is None:
+        torch = _torch()
+        if getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)() == device.index:
+            return _HERE_ALREADY
     return _on(device, stream)
 
 
