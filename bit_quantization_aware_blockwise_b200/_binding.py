@@ -697,9 +697,10 @@ def weight_grad(grad_y, codes, scales, bits: int, code_mode: int = CODES_PACKED,
     """grad_w = H (m * (grad_y^T @ x_hat)) / sqrt(128) per 128-column block, with x_hat = bf16((q + 1/2)
     Delta) read from the layer input's saved codes: grad_y bf16 [T, N] (unit column stride),
     codes as quantize_fwd or quantize_operands wrote them for [T, K] values (K is taken from a
-    2-D ``codes``), scales fp32 [T, K/128] or one step per token, mask = the weight's trust mask
-    bits [N, K/8] or None. Returns [N, K] in ``out_dtype`` (bfloat16 by default, or
-    float32). ``accumulate`` adds into a float32 ``out``."""
+    2-D ``codes``), scales fp32
+    [T, K/128] or one step per token, mask = the weight's trust mask bits [N, K/8] (not its byte
+    form) or None. Returns [N, K] in ``out_dtype`` (bfloat16 by default, or float32). ``accumulate``
+    adds into a float32 ``out``."""
     torch = _torch()
     _require_cuda(grad_y, "grad_y")
     dev = grad_y.device
@@ -720,8 +721,8 @@ def weight_grad(grad_y, codes, scales, bits: int, code_mode: int = CODES_PACKED,
     group = _rms_group("scales", scales, T, K) if T > 0 else K
     if mask is not None:
         _dense("mask", mask, (torch.uint8, torch.int32), dev)
-        if mask.numel() * mask.element_size() < N * K // 8:
-            raise QuestError("mask must hold N * K / 8 bytes")
+        if N * K > 0 and mask.numel() * mask.element_size() != N * K // 8:
+            raise QuestError(f"mask must hold the {N * K // 8} bytes of [N, K] mask bits, not {list(mask.shape)}")
     if accumulate and out is None:
         raise QuestError("accumulate needs out")
     dtype = out_dtype if out_dtype is not None else (out.dtype if out is not None else torch.bfloat16)

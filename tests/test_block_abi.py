@@ -134,3 +134,28 @@ def test_workspace_query_of_impossible_sizes():
     assert q.weight_grad_workspace(BIG, 8, BIG) == 0
     assert q.weight_grad_workspace(8, BIG, BIG) == 0
     assert q.weight_grad_workspace(1 << 29, 8, 1 << 14) >= 1 << 44
+
+
+def host_weight_grad(monkeypatch, T=4, N=16, width=256, **kw):
+    """weight_grad on host tensors, up to its library call (which is recorded, not made)."""
+    made = []
+    monkeypatch.setattr(q._binding, "_require_cuda", lambda t, name: None)
+    monkeypatch.setattr(q._binding, "_at", lambda device, stream: q._binding._HERE_ALREADY)
+    monkeypatch.setattr(q._binding, "_stream_handle", lambda stream, device: 0)
+    monkeypatch.setattr(q._binding, "weight_grad_raw", lambda *a, **k: made.append(a))
+    args = dict(codes=torch.zeros((T, width), dtype=torch.int8), scales=torch.ones((T, width // 128)), bits=8)
+    args.update(kw)
+    q.weight_grad(torch.zeros((T, N), dtype=torch.bfloat16), args.pop("codes"), args.pop("scales"), args.pop("bits"), **args)
+    assert len(made) == 1
+
+
+def test_weight_grad_takes_mask_bits_only(monkeypatch):
+    host_weight_grad(monkeypatch, mask=torch.zeros((16, 32), dtype=torch.uint8))
+    host_weight_grad(monkeypatch, mask=torch.zeros((16, 8), dtype=torch.int32))
+    host_weight_grad(monkeypatch, mask=torch.zeros(16 * 32, dtype=torch.uint8))
+    # the quantizer's other mask form, one byte a value, holds the bytes of eight masks of bits
+    for mask in (torch.ones((16, 256), dtype=torch.uint8), torch.ones(17 * 32, dtype=torch.uint8),
+                 torch.ones(15 * 32, dtype=torch.uint8)):
+        with pytest.raises(q.QuestError, match="mask"):
+            host_weight_grad(monkeypatch, mask=mask)
+
