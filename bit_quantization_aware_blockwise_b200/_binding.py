@@ -697,7 +697,7 @@ def weight_grad(grad_y, codes, scales, bits: int, code_mode: int = CODES_PACKED,
     """grad_w = H (m * (grad_y^T @ x_hat)) / sqrt(128) per 128-column block, with x_hat = bf16((q + 1/2)
     Delta) read from the layer input's saved codes: grad_y bf16 [T, N] (unit column stride),
     codes as quantize_fwd or quantize_operands wrote them for [T, K] values (K is taken from a
-    2-D ``codes``), scales fp32
+    2-D ``codes``, one row a token; a flat one may go on behind the last token), scales fp32
     [T, K/128] or one step per token, mask = the weight's trust mask bits [N, K/8] (not its byte
     form) or None. Returns [N, K] in ``out_dtype`` (bfloat16 by default, or float32). ``accumulate``
     adds into a float32 ``out``."""
@@ -716,8 +716,8 @@ def weight_grad(grad_y, codes, scales, bits: int, code_mode: int = CODES_PACKED,
             raise QuestError("K is needed unless codes is 2-D with a row per token")
         K = codes.shape[1] * 8 // per
     K = int(K)
-    if codes.numel() < T * K * per // 8:
-        raise QuestError(f"codes must hold {K * per // 8} bytes per token")
+    if codes.numel() < T * K * per // 8 or (codes.dim() == 2 and codes.shape != (T, K * per // 8)):
+        raise QuestError(f"codes must hold {K * per // 8} bytes for each of {T} tokens, not {list(codes.shape)}")
     group = _rms_group("scales", scales, T, K) if T > 0 else K
     if mask is not None:
         _dense("mask", mask, (torch.uint8, torch.int32), dev)

@@ -159,3 +159,14 @@ def test_weight_grad_takes_mask_bits_only(monkeypatch):
         with pytest.raises(q.QuestError, match="mask"):
             host_weight_grad(monkeypatch, mask=mask)
 
+
+def test_weight_grad_codes_rows(monkeypatch):
+    host_weight_grad(monkeypatch, codes=torch.zeros(4 * 256, dtype=torch.int8), K=256)
+    host_weight_grad(monkeypatch, codes=torch.zeros(9 * 256, dtype=torch.int8), K=256)      # rows behind the last token
+    host_weight_grad(monkeypatch, codes=torch.zeros((4, 128), dtype=torch.uint8), bits=4, K=256)
+    for codes, kw in ((torch.zeros((4, 384), dtype=torch.int8), dict(K=256)),               # longer rows than K
+                      (torch.zeros((5, 256), dtype=torch.int8), dict(K=256)),               # another token count
+                      (torch.zeros((4, 256), dtype=torch.uint8), dict(K=256, bits=4)),      # not packed
+                      (torch.zeros(3 * 256, dtype=torch.int8), dict(K=256))):
+        with pytest.raises(q.QuestError, match="codes"):
+            host_weight_grad(monkeypatch, codes=codes, **kw)
