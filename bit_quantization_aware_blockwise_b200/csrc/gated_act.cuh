@@ -35,8 +35,10 @@ __device__ __forceinline__ float gate_slope(float a, float s) {
 }
 
 // 8-bit checkpoint of a group of up to 128 consecutive columns of a row: Delta = max|v| / 128,
-// q = floor(v / Delta), restored as (q + 1/2) Delta, the midrise form of the quantizer's codes; the error
-// is at most Delta / 2 everywhere, the group's largest value included. Magnitudes are compared as
+// q = floor(v / Delta), restored as (q + 1/2) Delta, the midrise form of the quantizer's codes. The quotient is
+// v * inv with inv 1.5 2^-22 below 1 / Delta at most (ckpt_scale), so a value at k Delta, |k| <= 128, counts as below
+// the boundary up to 1.5 2^-15 Delta above it; with the restored product's rounding, 2^-17 Delta, the error is at
+// most (1/2 + 2^-14) Delta everywhere, the group's largest value included. Magnitudes are compared as
 // bit patterns, so that a NaN wins and the whole group restores to NaN (an infinity: to infinities).
 constexpr float kCkptMagic = 12582912.0f;   // 1.5 * 2^23: x + magic holds floor(x) in its low bits under rounding down
 

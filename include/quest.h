@@ -448,7 +448,8 @@ quest_status quest_transpose_bf16(const void* src, int64_t rows, int64_t cols, v
  * of each projection:
  *     Delta = max|v| / 128,  q = floor(v / Delta) in [-128, 127],  restored (q + 1/2) Delta,
  * the midrise form of the quantizer's codes without a clip: no value is off by more than
- * Delta / 2 (and Delta 2^-22 for a value next to a boundary). A group whose largest magnitude is below
+ * (1/2 + 2^-14) Delta (the quotient is taken up to 1.5 2^-22 low, which for a quotient of up to 128 moves a boundary
+ * by up to 2^-14.4, and the restored product rounds). A group whose largest magnitude is below
  * 2^-100 is kept as zeros; a group that holds an Inf or a NaN is restored to non-finite
  * values throughout.
  *
