@@ -33,7 +33,8 @@ namespace {
 //
 // E2M1 codes become fp16 pairs by the hardware conversion (as fast as a logic instruction, two codes each)
 // and take m16n8k16 with fp32 sums; x is rounded to fp16 under a power of two per token and group
-// that puts its largest value into [2^14, 2^15): 2^-12 of each value.
+// that puts its largest value into [2^14, 2^15): off by half a step, 2^-11 of each value, or where fp16 is
+// subnormal 2^-25, which is 2^-39 of the largest.
 //
 // Columns may be permuted freely as long as both operands agree: lane (g, t) of a warp takes the 32
 // codes 32t .. 32t+31 of a 128-column group of rows g and g + 8, and x's fragments are laid out to match.

@@ -545,8 +545,8 @@ size_t quest_weight_grad_workspace(int64_t T, int64_t N, int64_t K);
  * with v = q + 1/2 (QUEST_CODES_PACKED, the 4-bit containers of bits 3 and 4) or the E2M1
  * value (QUEST_CODES_FP4_PACKED). xt is rounded once, per token and 128 columns: to 16-bit fixed
  * point for the midrise codes (off by at most 2^-16 of the group's largest value) and to fp16 under a
- * power of two for E2M1 (2^-12 of each value); a group whose largest value is below about 2^-100
- * counts as zero. A group's sum is
+ * power of two for E2M1 (off by at most 2^-11 of each value, and 2^-39 of the group's largest where that is more);
+ * a group whose largest value is below about 2^-100 counts as zero. A group's sum is
  * exact (midrise) or fp32, the sum over groups fp32. A token that holds an Inf or a NaN gives
  * non-finite results, its own only.
  *

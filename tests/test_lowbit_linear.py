@@ -279,3 +279,41 @@ def test_two_weights_in_turn_in_the_same_buffers(cuda_device, M, gated, rms):
         value, tol = want[i % 2]
         assert ((y.double() - value).abs() <= tol).all()
         assert torch.equal(y, outs[i % 2])
+
+
+def product_e2m1(x, w, had):
+    """x rounded to fp16 with its group's largest value A in [2^14, 2^15): half a step, 2^-11 of a value (11 bits), or
+    2^-25 <= 2^-39 A where fp16 is subnormal. Otherwise as product()."""
+    xt = ref.transform(x.double(), had)
+    top = xt.reshape(xt.shape[0], -1, 128).abs().amax(-1).repeat_interleave(128, 1)
+    e = torch.maximum(xt.abs() * 2 ** -11, top * 2 ** -39)
+    w2 = w.square().t()
+    return xt @ w.t(), 6 * (e.square() @ w2).sqrt() + 2 ** -17 * (xt.square() @ w2).sqrt() + 1e-38
+
+
+@pytest.mark.parametrize("M,N,K,had", [(3, 264, 1024, 128), (16, 136, 2048, 256)])
+def test_e2m1_input_rounding(cuda_device, M, N, K, had):
+    codes, scales, w = weight(N, K, "fp4", False, seed=27)
+    x = activations(M, K, seed=28)
+    got = q.lowbit_linear(x, codes, scales, code_mode=q.CODES_FP4_PACKED, had_block=had)
+    want, err = product_e2m1(x, w, had)
+    assert ((got.double() - want).abs() <= 2 ** -8 * want.abs() + err).all()
+
+
+@pytest.mark.parametrize("M", [2, 16])
+def test_e2m1_values_far_below_their_group(cuda_device, M):
+    # one value of each group 2^30 to 2^38 above the others and met by a zero weight, so that only the others show: below
+    # 2^-28 of the largest they are fp16 subnormals, with 2^-39 of the largest as their bound
+    N, K = 72, 512
+    codes, scales, _ = weight(N, K, "fp4", False, seed=29)
+    codes = codes.reshape(N, -1, 64)
+    codes[:, :, 0] &= 0xF0                               # column 0 of each group
+    w = ref.scaled(ref.e2m1(codes, N), scales)
+    assert not w.reshape(N, -1, 128)[:, :, 0].any()
+    g = gen(30)
+    x = torch.randn(M, K // 128, 128, device="cuda", generator=g)
+    x[:, :, 0] = torch.exp2(torch.randint(30, 39, (M, K // 128), device="cuda", generator=g).float())
+    x = x.reshape(M, K).to(BF)
+    got = q.lowbit_linear(x, codes.reshape(N, -1), scales, code_mode=q.CODES_FP4_PACKED, had_block=0)
+    want, err = product_e2m1(x, w, 0)                    # (the zero weights drop the large values from every sum)
+    assert ((got.double() - want).abs() <= 2 ** -8 * want.abs() + err).all()
