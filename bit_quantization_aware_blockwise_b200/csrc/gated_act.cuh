@@ -13,8 +13,10 @@ namespace {
 
 // act(a) = a s(a), s = sigmoid(z(a)): z = a (SiLU) or z = 2 sqrt(2/pi) (a + 0.044715 a^3)
 // (the tanh form of GELU, since (1 + tanh(u)) / 2 = sigmoid(2 u)). exp and the quotient are
-// the fast intrinsics (a few 1e-7 relative each, four orders below the bf16 outputs): exp
-// overflows to infinity for z < -88, where the quotient is 0 as it should be.
+// the fast intrinsics. Their error grows with the argument, about 2 + 1.2 |z| units in the last place: a few 1e-7 for
+// small |z|, up to 1.3e-5 (2^-16) for z near -87, where all of it reaches s, still 2^-8 of the bf16 outputs' rounding.
+// The quotient is 0 for a divisor above 2^126, so s is 0 from z < -87.3 on, off by at most 2^-126; exp overflows
+// to infinity for z < -88.7, where the quotient is 0 as it should be.
 constexpr float kGeluZ = 1.5957691216057308f;   // 2 sqrt(2 / pi)
 constexpr float kGeluC = 0.044715f;
 

@@ -252,3 +252,26 @@ def test_streams_graphs_and_repeats(cuda_device):
     torch.cuda.synchronize()
     assert torch.equal(hg, h) and torch.equal(gg, grad)
     q.device_status()
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+def test_forward_with_steep_negative_gates(cuda_device, act):
+    # gates down to where the sigmoid leaves fp32's normal range: exp's error there is about 104 units in the last place
+    # (2^-16), and a quotient below 2^-126 is 0. x is one-hot and up is 1, so the projections are exact
+    F, K = 256, 64
+    wg = torch.zeros(F, K, device="cuda")
+    top = 95.0 if act == "silu" else 11.0                # z = -(95, and 1.6 (11 + 0.0447 1331) = 113)
+    wg[:, 0] = -torch.linspace(1.0, top, F, device="cuda")
+    wu = torch.zeros(F, K, device="cuda")
+    wu[:, 0] = 1
+    x = torch.zeros(2, K, device="cuda")
+    x[:, 0] = 1
+    x, wg, wu = x.to(BF), wg.to(BF), wu.to(BF)
+    h = q.gated_linear(x, wg, wu, act=act)
+    q.device_status()
+    a = wg[:, 0].double()
+    want = ref.gate(a, act)[0]
+    # GELU's own exponent z is a product of fp32 roundings, 2 2^-23 of |z|, which exp turns into as much of the value
+    z = 0.0 if act == "silu" else 113 * 2 * 2 ** -23
+    tol = (2 ** -8 + 2 ** -16 + z) * want.abs() + 2.0 ** -126 * a.abs() + 2.0 ** -133
+    assert ((h[0].double() - want).abs() <= tol).all() and torch.equal(h[0], h[1])
