@@ -228,3 +228,30 @@ def test_streams_and_graphs(cuda_device):
     for _, out in graphs:
         assert torch.equal(out, want2)
     q.device_status()
+
+
+@pytest.mark.parametrize("kind", ["int8", "packed4"])
+def test_bf16_gradient_over_several_accumulator_segments(cuda_device, kind):
+    # uncut tokens, more output tiles than CTA pairs and three segments (4096 + 4096 + 8 tokens): the sums meet in the
+    # epilogue's registers, and the accumulators' parity carries from tile to tile
+    T, N, K = 8200, 2568, 2176
+    assert q.weight_grad_workspace(T, N, K) < 2 * T * K + 256
+    gy, mask = grad_and_mask(T, N, K, seed=40)
+    codes, scales, xh, bits, mode = saved(T, K, kind, False, seed=41)
+    check(q.weight_grad(gy, codes, scales, bits, code_mode=mode, mask=mask), gy, xh, mask, T)
+    q.device_status()
+
+
+@pytest.mark.parametrize("T,N,K,split", [(4096, 2568, 2176, False), (4096, 264, 256, True), (8200, 2568, 2176, False)])
+def test_fp32_gradient_keeps_the_precision_of_its_segments(cuda_device, T, N, K, split):
+    # A tensor-core addition cuts the running sum toward zero, by half of 2^-23 of it on average, and the sum of
+    # zero-mean terms grows as the root of their number, 2/3 of its end on average: 32 additions of 16 tokens a segment
+    # give 32 2^-24 2/3 = 1.3e-6 of a segment's sum, and of the whole, whose segments add up like their errors.
+    # Without segments 4096 tokens are 256 additions: 1.0e-5 by the same count (4.3e-6 measured)
+    assert (q.weight_grad_workspace(T, N, K) >= 2 * T * K + 256) == split
+    gy, mask = grad_and_mask(T, N, K, seed=42)
+    codes, scales, xh, bits, mode = saved(T, K, "int8", False, seed=43)
+    got = q.weight_grad(gy, codes, scales, bits, code_mode=mode, mask=mask, out_dtype=torch.float32)
+    q.device_status()
+    want = ref.weight_grad(gy, xh, mask)
+    assert (got.double() - want).norm() <= 1.5e-6 * want.norm()
