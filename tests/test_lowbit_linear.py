@@ -317,3 +317,19 @@ def test_e2m1_values_far_below_their_group(cuda_device, M):
     got = q.lowbit_linear(x, codes.reshape(N, -1), scales, code_mode=q.CODES_FP4_PACKED, had_block=0)
     want, err = product_e2m1(x, w, 0)                    # (the zero weights drop the large values from every sum)
     assert ((got.double() - want).abs() <= 2 ** -8 * want.abs() + err).all()
+
+
+@pytest.mark.parametrize("M", [1, 9, 40])
+def test_three_bit_codes_in_four_bit_containers(cuda_device, M):
+    W = (torch.randn(264, 640, device="cuda", generator=gen(31)) * 0.02).to(BF)
+    x = activations(M, 640, seed=32)
+    for rms in (128, 640):
+        qw = q.quantize_fwd(W, 3, rms_group=rms, mask_mode=None, dequant="fp32")
+        w = ref.scaled(ref.midrise4(qw["codes"], 264), qw["scales"])
+        assert w.abs().max() <= 3.5 * qw["scales"].double().max()      # (in 64 bits, where 3.5 Delta is exact)
+        check_linear(q.lowbit_linear(x, qw["codes"], qw["scales"]), x, w, 128)
+        a, ea = product(x, w, 128, "int4")
+        v, _ = ref.gate(a, "silu")
+        got = q.lowbit_gated(x, qw["codes"], qw["scales"], qw["codes"], qw["scales"])
+        tol = (2 ** -8 + 2 ** -16) * (v * a).abs() + 1.13 * ea * (a.abs() + ea) + v.abs() * ea + 1e-38
+        assert ((got.double() - v * a).abs() <= tol).all()

@@ -255,3 +255,39 @@ def test_fp32_gradient_keeps_the_precision_of_its_segments(cuda_device, T, N, K,
     q.device_status()
     want = ref.weight_grad(gy, xh, mask)
     assert (got.double() - want).norm() <= 1.5e-6 * want.norm()
+
+
+@pytest.mark.parametrize("bits", [3, 5, 6, 7])
+@pytest.mark.parametrize("rows", [False, True])
+def test_packed_codes_of_every_width(cuda_device, bits, rows):
+    # the quantizer's own packed codes: 3 bits in 4-bit containers, 5 to 7 in bytes; x_hat is its dequant but for ties
+    T, N, K = 200, 136, 384
+    gy, mask = grad_and_mask(T, N, K, seed=44)
+    X = torch.randn(T, K, device="cuda", generator=gen(45)).to(BF)
+    qx = q.quantize_fwd(X, bits, rms_group=K if rows else 128, mask_mode=None, dequant="fp32")
+    values = (ref.midrise4(qx["codes"], T) if bits == 3 else qx["codes"].view(torch.int8).view(T, K).double() + 0.5)
+    xh = ref.bf16_input(values, qx["scales"])
+    assert (xh - qx["dequant"].double()).abs().max() <= 2 ** -8 * qx["dequant"].abs().max()
+    got = q.weight_grad(gy, qx["codes"], qx["scales"], bits, mask=mask, K=K, out_dtype=torch.float32)
+    q.device_status()
+    check(got, gy, xh, mask, T)
+
+
+@pytest.mark.parametrize("form", ["midrise", "fp4"])
+@pytest.mark.parametrize("rows", [False, True])
+def test_operand_codes_of_the_quantizer(cuda_device, form, rows):
+    # the int8 operand bytes c of the linear layers, x_hat = bf16(c Delta / 2): 2 q + 1, and twice the E2M1 value
+    T, N, K = 130, 264, 256
+    gy, mask = grad_and_mask(T, N, K, seed=46)
+    X = torch.randn(T, K, device="cuda", generator=gen(47)).to(BF)
+    mode = q.CODES_GEMM_OPERAND if form == "midrise" else q.CODES_FP4_OPERAND
+    qx = q.quantize_fwd(X, 4, rms_group=K if rows else 128, code_mode=mode, mask_mode=None, dequant="fp32")
+    c = qx["codes"].view(torch.int8).view(T, K)
+    if form == "fp4":
+        assert set(c.abs().unique().tolist()) <= {0, 1, 2, 3, 4, 6, 8, 12}
+    xh = ref.bf16_input(c.double() / 2, qx["scales"])
+    assert (xh - qx["dequant"].double()).abs().max() <= 2 ** -8 * qx["dequant"].abs().max()
+    for out in (BF, torch.float32):
+        got = q.weight_grad(gy, c, qx["scales"], 4, code_mode=mode, mask=mask, out_dtype=out)
+        q.device_status()
+        check(got, gy, xh, mask, T)
