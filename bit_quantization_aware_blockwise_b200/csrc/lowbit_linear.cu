@@ -281,8 +281,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) lowbit_kernel(const LowbitPara
     extern __shared__ __align__(256) uint8_t lsmem[];
     constexpr int MATS = GATED ? 2 : 1, TOK = 8 * NT;
     // Pairs of groups in registers (of each matrix), and per turn of the loop, as registers allow. One matrix, up to 8
-    // tokens: 44032 x 8192 took 59, 54 and 51 us with 1, 2 and 4; 16 tokens x 8192 x 22016: 41, 40 and 56. Two matrices:
-    // 22016 x 8192 took 52 us with one of each, 61 with two.
+    // tokens: 44032 x 8192 took 61, 55 and 52 us with 1, 2 and 4; 16 tokens x 8192 x 22016: 45.6, 45.5 and 62. Two matrices:
+    // 5 x 22016 x 8192 took 53 us with one of each, 60 with two.
     constexpr int kPairs = GATED ? 1 : NT == 1 ? 4 : 2;
     static_assert(kChunk % (2 * kPairs) == 0, "a turn lies in one chunk of scales");
     constexpr int kTile = MATS * TOK * 16;   // one tile's sums, [matrix][token][row]

@@ -27,7 +27,7 @@ namespace {
 // rare ties): 3 bytes moved per value. The product then runs at the tensor cores' rate. Restoring inside
 // the product's mainloop instead repeats the work for every 256 rows of G: eight conversion warps
 // beside the MMAs took 694 us at 16384 x 11264 x 2048 (541 with the conversion's arithmetic and stores
-// taken out) where the pass costs 20 us and all of it 502.
+// taken out) where the pass costs 20 us and all of it 502 (single calls; 599-647 back to back, as the power cap settles).
 //
 // The reduction runs over the tokens, the outer dimension of both operands, so the MMA
 // takes both transposed (MN-major): a stage row is one token's 64 columns (128 bytes,
