@@ -333,3 +333,23 @@ def test_three_bit_codes_in_four_bit_containers(cuda_device, M):
         got = q.lowbit_gated(x, qw["codes"], qw["scales"], qw["codes"], qw["scales"])
         tol = (2 ** -8 + 2 ** -16) * (v * a).abs() + 1.13 * ea * (a.abs() + ea) + v.abs() * ea + 1e-38
         assert ((got.double() - v * a).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("grid", ["int4", "fp4"])
+@pytest.mark.parametrize("had", [0, 128, 256])
+@pytest.mark.parametrize("M", [4, 40])
+def test_non_finite_tokens_stay_alone_in_every_form(cuda_device, M, had, grid):
+    # untransformed too, where an infinity meets zero weights; transformed by the layer's kernel and by one of its own
+    N, K = 72, 1024
+    codes, scales, w = weight(N, K, grid, False, seed=33)
+    x = activations(M, K, seed=34)
+
+    def both(v):
+        return (q.lowbit_linear(v, codes, scales, code_mode=mode(grid), had_block=had),
+                q.lowbit_gated(v, codes, scales, codes, scales, code_mode=mode(grid), had_block=had))
+    clean = both(x)
+    x[1, 7], x[M - 1, 300] = float("-inf"), float("nan")
+    keep = [m for m in range(M) if m not in (1, M - 1)]
+    for got, was in zip(both(x), clean):
+        assert torch.equal(got[keep], was[keep])
+    assert not both(x)[0][[1, M - 1]].isfinite().any()
