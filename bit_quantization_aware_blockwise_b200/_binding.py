@@ -631,9 +631,10 @@ def _pitch(t):
 
 def _rms_group(name, scales, rows, K):
     """128 or K, read off a [rows, K / rms_group] (or, one step per row, [rows]) scale tensor."""
-    if scales.numel() == rows and K != 128:
+    one_each = scales.numel() == rows and scales.dim() > 0 and scales.shape[0] == rows
+    if one_each and K != 128:
         return K
-    if K % 128 == 0 and tuple(scales.shape) == (rows, K // 128) or scales.numel() == rows:
+    if K % 128 == 0 and tuple(scales.shape) == (rows, K // 128) or one_each:
         return 128
     raise QuestError(f"{name} must be [{rows}, {K // 128}] or one step per row, not {list(scales.shape)}")
 

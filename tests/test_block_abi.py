@@ -170,3 +170,12 @@ def test_weight_grad_codes_rows(monkeypatch):
                       (torch.zeros(3 * 256, dtype=torch.int8), dict(K=256))):
         with pytest.raises(q.QuestError, match="codes"):
             host_weight_grad(monkeypatch, codes=codes, **kw)
+
+
+def test_steps_of_another_row_count(monkeypatch):
+    for scales in (torch.ones((4, 2)), torch.ones((4, 1)), torch.ones(4)):
+        host_weight_grad(monkeypatch, scales=scales)
+    # as many numbers as tokens, but two groups for each of two tokens
+    for scales in (torch.ones((2, 2)), torch.ones((1, 4)), torch.ones((3, 2)), torch.ones(())):
+        with pytest.raises(q.QuestError, match="scales"):
+            host_weight_grad(monkeypatch, scales=scales)
