@@ -639,6 +639,12 @@ def _rms_group(name, scales, rows, K):
     raise QuestError(f"{name} must be [{rows}, {K // 128}] or one step per row, not {list(scales.shape)}")
 
 
+def _rows(name, scales):
+    if scales.dim() == 0:
+        raise QuestError(f"{name} must have a row for each row of the weight")
+    return scales.shape[0]
+
+
 def gated_linear(x_hat, w_gate, w_up, act="silu", checkpoint: bool = False, out=None, stream=None):
     """h = act(x_hat @ w_gate^T) * (x_hat @ w_up^T), the gated feed-forward block up to its down
     projection: x_hat bf16 [M, K], weights bf16 [F, K], h bf16 [M, F]; act "silu" or
@@ -753,7 +759,7 @@ def lowbit_linear(x, w_codes, w_scales, code_mode: int = CODES_PACKED, had_block
     dev = x.device
     _dense("x", x, (torch.bfloat16,), dev, pitched=True)
     M, K = x.shape
-    N = w_scales.shape[0]
+    N = _rows("w_scales", w_scales)
     _lowbit_weight("w", w_codes, w_scales, N, K, dev)
     group = _rms_group("w_scales", w_scales, N, K) if N > 0 else K
     with _at(dev, stream):
@@ -785,7 +791,7 @@ def lowbit_gated(x, gate_codes, gate_scales, up_codes, up_scales, act="silu", co
     dev = x.device
     _dense("x", x, (torch.bfloat16,), dev, pitched=True)
     M, K = x.shape
-    F = gate_scales.shape[0]
+    F = _rows("gate_scales", gate_scales)
     _lowbit_weight("gate", gate_codes, gate_scales, F, K, dev)
     _lowbit_weight("up", up_codes, up_scales, F, K, dev)
     group = _rms_group("gate_scales", gate_scales, F, K) if F > 0 else K

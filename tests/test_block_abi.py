@@ -179,3 +179,11 @@ def test_steps_of_another_row_count(monkeypatch):
     for scales in (torch.ones((2, 2)), torch.ones((1, 4)), torch.ones((3, 2)), torch.ones(())):
         with pytest.raises(q.QuestError, match="scales"):
             host_weight_grad(monkeypatch, scales=scales)
+
+
+def test_low_bit_steps_without_rows(monkeypatch):
+    monkeypatch.setattr(q._binding, "_require_cuda", lambda t, name: None)
+    x, codes, s = torch.zeros((1, 128), dtype=torch.bfloat16), torch.zeros(64, dtype=torch.uint8), torch.ones(())
+    for call in (lambda: q.lowbit_linear(x, codes, s), lambda: q.lowbit_gated(x, codes, s, codes, s)):
+        with pytest.raises(q.QuestError, match="scales"):
+            call()
